@@ -8,6 +8,10 @@ HIP kernels.  PyTorch supplies device memory and the stream.
     out = gemm_rs(A, B, partials, ws, R=8, rank=5)        # GEMM-RS
     out = ag_gemm(A, B, shards, flags, status, R=8, rank=3, epoch=1)
 
+The routed and grouped operators of include/gemm_coll_grouped.h (expert
+router, grouped products, combine, adapters) are in .grouped and reached from
+here too.
+
 Tensors are bf16, contiguous, on the current CUDA (HIP) device.  By default
 each call uses a workspace that lets the kernel split leftover tiles along
 K, allocated once per (device, stream) pair, so that calls in flight on
@@ -26,7 +30,8 @@ __all__ = ["gemm_ar", "gemm_ar_noalloc", "gemm_rs", "gemm_ar_two_shot", "ag_gemm
            "lib", "GcPeers", "GcPlan",
            "workspace_bytes", "default_workspace",
            "LIB_PATH", "GC_OK", "GC_EINVAL", "GC_ENOTSUP", "GC_EIO", "GC_ENOSPC",
-           "GC_TIMEOUT_BASE"]
+           "GC_TIMEOUT_BASE",
+           "moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm_coll.so")
 
@@ -104,6 +109,8 @@ def lib() -> ctypes.CDLL:
                                      ctypes.c_int, ctypes.c_int, ctypes.c_uint32,
                                      ctypes.POINTER(GcPlan)]
         L.gemm_coll_plan.restype = ctypes.c_int
+        from .grouped import declare
+        declare(L)
         _lib = L
     return _lib
 
@@ -380,3 +387,15 @@ def ag_push_shards(src, dst, flags, epoch_word, *, R: int, rank: int, stream=Non
     _check(lib().ag_push_shards(_ptr(src), _ptr(dst), Ms, K, R, rank, _ptr(flags), _ptr(epoch_word),
                                 _stream(stream)), "ag_push_shards")
 
+
+_GROUPED = ("moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add", "Routing", "Groups",
+            "grouped_workspace_bytes", "lora_workspace_bytes")
+
+
+def __getattr__(name):
+    """The routed and grouped operators, from .grouped (which needs torch) on first use."""
+    if name in _GROUPED:
+        from . import grouped
+        globals().update({n: getattr(grouped, n) for n in _GROUPED})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

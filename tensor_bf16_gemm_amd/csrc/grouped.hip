@@ -1,0 +1,391 @@
+// grouped.hip -- host side of the C ABI declared in include/gemm_coll_grouped.h:
+// argument validation, choice of the kernel instance, launches.
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "combine.hpp"
+#include "gemm_coll_grouped.h"
+#include "grouped.hpp"
+#include "lora.hpp"
+#include "route.hpp"
+
+static_assert(GC_GROUPS_MAX == gc::RT_GROUPS && GC_GROUPS_MAX == gc::GR_GROUPS, "groups");
+static_assert(GC_TOPK_MAX == gc::RT_TOP, "k");
+static_assert(GC_SCORE_SOFTMAX == gc::SCORE_SOFTMAX && GC_SCORE_SIGMOID == gc::SCORE_SIGMOID, "scores");
+
+namespace {
+
+constexpr int kMaxDevices = 64;
+std::atomic<int> g_cus[kMaxDevices];      // 0 = not queried yet
+
+int cu_count(int &cus)
+{
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess)
+        return GC_EIO;
+    cus = dev < kMaxDevices ? g_cus[dev].load(std::memory_order_relaxed) : 0;
+    if (cus == 0) {
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+            cus <= 0)
+            return GC_EIO;
+        if (dev < kMaxDevices)
+            g_cus[dev].store(cus, std::memory_order_relaxed);
+    }
+    return GC_OK;
+}
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool good16(const void *p) { return p && aligned(p, 16); }
+bool good4(const void *p) { return p && aligned(p, 4); }
+
+// Buffers are addressed through 32-bit byte offsets with an out-of-range
+// sentinel at 2^31.
+bool fits(int64_t rows, int64_t cols) { return cols == 0 || rows < ((int64_t)1 << 30) / cols; }
+
+// Workspace: arrival counters (one per workgroup of the streaming kernel),
+// then partial tiles, two of at most kPartBytes per workgroup.  The many-block
+// grouping keeps its counts where the partial tiles are, and lora_add its
+// middle activations behind them.
+constexpr int64_t kCountBytes = 4096;
+constexpr int64_t kPartBytes = 32768;
+constexpr int kMaxWorkers = (int)(kCountBytes / 4);
+
+int workers(int cus) { return std::min(cus, kMaxWorkers); }
+int64_t base_bytes(int cus) { return kCountBytes + 2 * kPartBytes * workers(cus); }
+
+int launched() { return hipGetLastError() == hipSuccess ? GC_OK : GC_EIO; }
+
+template <bool BF16, bool ONE>
+void launch_route(const gc::RouteArgs &a, int vpl, int blocks, hipStream_t st)
+{
+    const dim3 g(blocks), b(gc::RT_THREADS);
+    switch (vpl) {
+    case 1: hipLaunchKernelGGL((gc::route_kernel<1, BF16, ONE>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gc::route_kernel<2, BF16, ONE>), g, b, 0, st, a); break;
+    case 4: hipLaunchKernelGGL((gc::route_kernel<4, BF16, ONE>), g, b, 0, st, a); break;
+    case 8: hipLaunchKernelGGL((gc::route_kernel<8, BF16, ONE>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((gc::route_kernel<16, BF16, ONE>), g, b, 0, st, a); break;
+    }
+}
+
+// Routing (vpl > 0) and grouping of a.T * a.k items.
+int route_and_group(gc::RouteArgs &a, int vpl, bool bf16, void *workspace, uint64_t bytes,
+                    hipStream_t st)
+{
+    const int64_t items = (int64_t)a.T * a.k;
+    if (items <= gc::ROUTE_ONE_ITEMS) {
+        if (vpl == 0)
+            hipLaunchKernelGGL((gc::route_kernel<0, false, true>), dim3(1), dim3(gc::RT_THREADS), 0, st, a);
+        else if (bf16)
+            launch_route<true, true>(a, vpl, 1, st);
+        else
+            launch_route<false, true>(a, vpl, 1, st);
+        return launched();
+    }
+    // Blocks of consecutive tokens: about 512 items each, at most RT_BLOCKS.
+    const int64_t per = std::max<int64_t>({1, 512 / a.k, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS});
+    const int blocks = (int)((a.T + per - 1) / per);
+    a.block_tokens = (int)per;
+    a.cstride = (a.E + 1 + 7) / 8 * 8;
+    if (a.offsets) {
+        if (!good16(workspace) || bytes < (uint64_t)(kCountBytes + (int64_t)blocks * a.cstride * 2))
+            return GC_EINVAL;
+        a.counts = (uint16_t *)((char *)workspace + kCountBytes);
+    }
+    if (vpl == 0)
+        hipLaunchKernelGGL((gc::route_kernel<0, false, false>), dim3(blocks), dim3(gc::RT_THREADS), 0, st, a);
+    else if (bf16)
+        launch_route<true, false>(a, vpl, blocks, st);
+    else
+        launch_route<false, false>(a, vpl, blocks, st);
+    if (a.offsets)
+        hipLaunchKernelGGL(gc::place_kernel, dim3(blocks), dim3(gc::RT_THREADS), 0, st, a);
+    return launched();
+}
+
+template <int NB, int RB, int D, int EPI>
+void launch_stream(gc::GroupedArgs &a, int cus, hipStream_t st)
+{
+    const int64_t f = EPI == gc::EPI_GLU ? a.N / 2 : a.N, bn = EPI == gc::EPI_GLU ? 8 * NB : 16 * NB;
+    a.tiles_n = (int)((f + bn - 1) / bn);
+    const int grid = workers(cus);
+    a.part_slots = 2 * grid;
+    // A piece of fewer than 4 quads (16 K-steps) costs more to hand over than
+    // it saves; without a workspace no tile is cut at all.
+    const int kt = (a.K + gc::BK - 1) / gc::BK;
+    a.min_quads = a.part ? 4 : std::max(1, (kt + 3) / 4);
+    hipLaunchKernelGGL((gc::stream_kernel<NB, RB, D, EPI>), dim3(grid), dim3(gc::ST_THREADS), 0, st, a);
+}
+
+template <int NB, int EPI>
+void launch_stream_rows(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hipStream_t st)
+{
+    if (rows_per_group <= 16)
+        launch_stream<NB, 1, 4, EPI>(a, cus, st);
+    else if (rows_per_group <= 32)
+        launch_stream<NB, 2, 3, EPI>(a, cus, st);
+    else
+        launch_stream<NB, 4, 3, EPI>(a, cus, st);
+}
+
+template <int RB>
+void launch_expand(const gc::ExpandArgs &a, int grid, hipStream_t st)
+{
+    const dim3 g(grid), b(gc::EX_THREADS);
+    switch ((a.r + 31) / 32) {
+    case 1: hipLaunchKernelGGL((gc::expand_kernel<RB, 1>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gc::expand_kernel<RB, 2>), g, b, 0, st, a); break;
+    case 3: hipLaunchKernelGGL((gc::expand_kernel<RB, 3>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((gc::expand_kernel<RB, 4>), g, b, 0, st, a); break;
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t gemm_coll_grouped_workspace_bytes(void)
+{
+    int cus = 0;
+    const int err = cu_count(cus);
+    return err ? err : base_bytes(cus);
+}
+
+int64_t gemm_coll_lora_workspace_bytes(int64_t M, int r)
+{
+    if (M < 0 || r < 0)
+        return GC_EINVAL;
+    int cus = 0;
+    const int err = cu_count(cus);
+    return err ? err : base_bytes(cus) + 2 * (M * r * 2 + 255) / 256 * 256;
+}
+
+int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int64_t T, int E, int k,
+                        int score, const float *bias, int renormalize, float scale, int32_t *ids,
+                        float *weights, int32_t *offsets, int32_t *rows, int32_t *slots,
+                        void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    if (T < 0 || E < 1 || E > GC_GROUPS_MAX || k < 1 || k > GC_TOPK_MAX || stride < E)
+        return GC_EINVAL;
+    if ((logits_type != GC_F32 && logits_type != GC_BF16) ||
+        (score != GC_SCORE_SOFTMAX && score != GC_SCORE_SIGMOID))
+        return GC_EINVAL;
+    const bool group = offsets || rows || slots;
+    if (group && (!good4(offsets) || (T > 0 && (!good4(rows) || !good4(slots)))))
+        return GC_EINVAL;
+    if (T > ((int64_t)1 << 24) / k)
+        return GC_ENOTSUP;
+    const uintptr_t elem = logits_type == GC_BF16 ? 2 : 4;
+    if (T > 0 && (!logits || !aligned(logits, elem) || !good4(ids) || !good4(weights)))
+        return GC_EINVAL;
+    if (bias && !aligned(bias, 4))
+        return GC_EINVAL;
+    if (T == 0 && !group)
+        return GC_OK;
+    int vpl = 1;
+    while (vpl * 64 < E)
+        vpl *= 2;
+    gc::RouteArgs a = {};
+    a.logits = logits;
+    a.stride = stride;
+    a.bias = bias;
+    a.T = (int)T;
+    a.E = E;
+    a.k = k;
+    a.score = score;
+    a.renorm = renormalize != 0;
+    a.scale = scale;
+    a.ids = ids;
+    a.weights = weights;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.slots = slots;
+    a.vec = E % vpl == 0 && stride % vpl == 0 && aligned(logits, std::min<uintptr_t>(16, vpl * elem));
+    return route_and_group(a, vpl, logits_type == GC_BF16, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32_t *offsets,
+                         int32_t *rows, int32_t *slots, void *workspace, uint64_t workspace_bytes,
+                         void *stream)
+{
+    if (T < 0 || k < 1 || groups < 1 || groups > GC_GROUPS_MAX || !good4(offsets))
+        return GC_EINVAL;
+    if (T > ((int64_t)1 << 24) / k)
+        return GC_ENOTSUP;
+    if (T > 0 && (!good4(ids) || !good4(rows) || !good4(slots)))
+        return GC_EINVAL;
+    gc::RouteArgs a = {};
+    a.T = (int)T;
+    a.E = groups;
+    a.k = k;
+    a.ids = const_cast<int32_t *>(ids);      // (only read: no routing)
+    a.offsets = offsets;
+    a.rows = rows;
+    a.slots = slots;
+    return route_and_group(a, 0, false, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const int32_t *offsets,
+                           const int32_t *rows, int64_t S, int64_t K, int64_t N, int E, int act,
+                           gc_bf16 *out, void *workspace, uint64_t workspace_bytes, void *stream)
+{
+    if (T < 0 || S < 0 || K < 0 || N < 0 || E < 1 || E > GC_GROUPS_MAX)
+        return GC_EINVAL;
+    if (act != GC_ACT_NONE && act != GC_ACT_SILU_GLU)
+        return GC_EINVAL;
+    if (K % 8 != 0 || N % (act == GC_ACT_SILU_GLU ? 16 : 8) != 0 || (!rows && T < S))
+        return GC_EINVAL;
+    if (T > INT32_MAX || S > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX)
+        return GC_ENOTSUP;
+    if (!fits(T, K) || !fits(K, N) || !fits(S, N))
+        return GC_ENOTSUP;
+    if (S == 0 || N == 0)
+        return GC_OK;
+    if (!good4(offsets) || (rows && !aligned(rows, 4)) || !good16(out))
+        return GC_EINVAL;
+    if (K > 0 && ((T > 0 && !good16(X)) || !good16(W)))
+        return GC_EINVAL;
+    int cus = 0;
+    if (int err = cu_count(cus))
+        return err;
+    gc::GroupedArgs a = {};
+    if (workspace) {
+        if (!good16(workspace) || workspace_bytes < (uint64_t)base_bytes(cus))
+            return GC_EINVAL;
+        a.count = (uint32_t *)workspace;
+        a.part = (float *)((char *)workspace + kCountBytes);
+    }
+    a.X = X;
+    a.W = W;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.out = out;
+    a.T = (int)T;
+    a.S = (int)S;
+    a.K = (int)K;
+    a.N = (int)N;
+    a.E = E;
+    const int64_t avg = (S + E - 1) / E;
+    if (act == GC_ACT_SILU_GLU)
+        launch_stream_rows<8, gc::EPI_GLU>(a, avg, cus, (hipStream_t)stream);
+    else
+        launch_stream_rows<8, gc::EPI_PLAIN>(a, avg, cus, (hipStream_t)stream);
+    return launched();
+}
+
+int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, const float *weights,
+                          int64_t T, int k, int64_t N, const gc_bf16 *partials, int npeers,
+                          int64_t peer_stride, gc_bf16 *out, void *stream)
+{
+    if (S < 0 || T < 0 || N < 0 || k < 1 || k > GC_TOPK_MAX || npeers < 0 || npeers > 15 || N % 8 != 0)
+        return GC_EINVAL;
+    if (S > INT32_MAX || T > INT32_MAX || N > INT32_MAX)
+        return GC_ENOTSUP;
+    if (T == 0 || N == 0)
+        return GC_OK;
+    if (!good4(slots) || !good4(weights) || !good16(out) || (S > 0 && !good16(Y)))
+        return GC_EINVAL;
+    if (npeers > 0 && (!good16(partials) || peer_stride % 8 != 0 || (npeers > 1 && peer_stride < T * N)))
+        return GC_EINVAL;
+    gc::CombineArgs a = {};
+    a.Y = Y;
+    a.slots = slots;
+    a.weights = weights;
+    a.partials = partials;
+    a.peer_stride = peer_stride;
+    a.out = out;
+    a.T = (int)T;
+    a.S = (int)S;
+    a.N = (int)N;
+    a.k = k;
+    a.npeers = npeers;
+    a.col_groups = (int)((N / 8 + 63) / 64);
+    a.items = T * a.col_groups;
+    const int64_t blocks = (a.items + gc::CB_WAVES - 1) / gc::CB_WAVES;
+    if (blocks > INT32_MAX)
+        return GC_ENOTSUP;
+    hipLaunchKernelGGL(gc::combine_kernel, dim3((unsigned)blocks), dim3(gc::CB_THREADS), 0,
+                       (hipStream_t)stream, a);
+    return launched();
+}
+
+int gemm_coll_lora_add(const gc_bf16 *base, const gc_bf16 *X, const gc_bf16 *down, const gc_bf16 *up,
+                       const float *scale, const int32_t *offsets, const int32_t *rows, int64_t M,
+                       int64_t K, int64_t N, int r, int G, gc_bf16 *out, void *workspace,
+                       uint64_t workspace_bytes, void *stream)
+{
+    if (M < 0 || K < 0 || N < 0 || r < 8 || r > 128 || G < 1 || G >= GC_GROUPS_MAX)
+        return GC_EINVAL;
+    if (K % 8 != 0 || N % 8 != 0 || r % 8 != 0)
+        return GC_EINVAL;
+    if (M > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX)
+        return GC_ENOTSUP;
+    if (!fits(M, K) || !fits(M, N) || !fits(M, r) || !fits(K, r) || !fits(r, N))
+        return GC_ENOTSUP;
+    if (M == 0 || N == 0)
+        return GC_OK;
+    if (!good16(base) || !good16(out) || !good16(up) || !good4(scale) || !good4(offsets) || !good4(rows))
+        return GC_EINVAL;
+    if (K > 0 && (!good16(X) || !good16(down)))
+        return GC_EINVAL;
+    int cus = 0;
+    if (int err = cu_count(cus))
+        return err;
+    const int64_t hb = (M * r * 2 + 255) / 256 * 256;
+    if (!good16(workspace) || workspace_bytes < (uint64_t)(base_bytes(cus) + 2 * hb))
+        return GC_EINVAL;
+    char *ws = (char *)workspace;
+    const hipStream_t st = (hipStream_t)stream;
+    gc::GroupedArgs a = {};
+    a.X = X;
+    a.W = down;
+    a.offsets = offsets;
+    a.rows = rows;
+    a.scale = scale;
+    a.out = (uint16_t *)(ws + base_bytes(cus));
+    a.out_lo = (uint16_t *)(ws + base_bytes(cus) + hb);
+    a.T = (int)M;
+    a.S = (int)M;
+    a.K = (int)K;
+    a.N = r;
+    a.E = G;
+    a.count = (uint32_t *)ws;
+    a.part = (float *)(ws + kCountBytes);
+    const int64_t avg = (M + G - 1) / G;
+    if (r <= 16)
+        launch_stream_rows<1, gc::EPI_SPLIT>(a, avg, cus, st);
+    else if (r <= 32)
+        launch_stream_rows<2, gc::EPI_SPLIT>(a, avg, cus, st);
+    else if (r <= 64)
+        launch_stream_rows<4, gc::EPI_SPLIT>(a, avg, cus, st);
+    else
+        launch_stream_rows<8, gc::EPI_SPLIT>(a, avg, cus, st);
+    gc::ExpandArgs x = {};
+    x.base = base;
+    x.out = out;
+    x.h = a.out;
+    x.h_lo = a.out_lo;
+    x.up = up;
+    x.offsets = offsets;
+    x.rows = rows;
+    x.M = (int)M;
+    x.N = (int)N;
+    x.r = r;
+    x.E = G;
+    x.copy = out != base;
+    x.tiles_n = (int)((N + gc::EX_COLS - 1) / gc::EX_COLS);
+    const int bm = avg >= 32 ? 64 : 16;
+    const int64_t tiles = std::min<int64_t>(M, (M + bm - 1) / bm + G) * x.tiles_n;
+    const int grid = (int)std::min<int64_t>(tiles, (int64_t)cus * 4);
+    if (bm == 64)
+        launch_expand<4>(x, grid, st);
+    else
+        launch_expand<1>(x, grid, st);
+    return launched();
+}
+
+}  // extern "C"
