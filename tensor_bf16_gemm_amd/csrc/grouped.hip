@@ -10,6 +10,7 @@
 #include "combine.hpp"
 #include "gemm_coll_grouped.h"
 #include "grouped.hpp"
+#include "grouped_tile.hpp"
 #include "lora.hpp"
 #include "route.hpp"
 
@@ -130,6 +131,13 @@ void launch_stream_rows(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hip
         launch_stream<NB, 2, 3, EPI>(a, cus, st);
     else
         launch_stream<NB, 4, 3, EPI>(a, cus, st);
+}
+
+template <bool GLU>
+void launch_tiles(gc::GroupedArgs &a, int cus, hipStream_t st)
+{
+    a.tiles_n = GLU ? (a.N / 2 + gc::BN / 2 - 1) / (gc::BN / 2) : (a.N + gc::BN - 1) / gc::BN;
+    hipLaunchKernelGGL((gc::tile_kernel<GLU>), dim3(cus), dim3(gc::NT), 0, st, a);
 }
 
 template <int RB>
@@ -270,7 +278,12 @@ int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const 
     a.N = (int)N;
     a.E = E;
     const int64_t avg = (S + E - 1) / E;
-    if (act == GC_ACT_SILU_GLU)
+    if (avg > 64) {
+        if (act == GC_ACT_SILU_GLU)
+            launch_tiles<true>(a, cus, (hipStream_t)stream);
+        else
+            launch_tiles<false>(a, cus, (hipStream_t)stream);
+    } else if (act == GC_ACT_SILU_GLU)
         launch_stream_rows<8, gc::EPI_GLU>(a, avg, cus, (hipStream_t)stream);
     else
         launch_stream_rows<8, gc::EPI_PLAIN>(a, avg, cus, (hipStream_t)stream);

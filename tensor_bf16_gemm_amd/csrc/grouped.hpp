@@ -263,7 +263,8 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
         // Steps of this wave: s0, s0 + 4, ... below s1.  Steps past the end
         // issue the same number of loads, out of range, so that the wait
         // counts stay constant.  Rows of W past K lie past the buffer; the
-        // A chunks past K are masked (they would read the next row).
+        // A chunks past K are masked (they would read the next row).  An offset
+        // of OOB plus a step's advance, below 2^31, is still out of range.
         const int s1 = min(ST_WAVES * kb, KT);
         auto issue = [&](int s, uint32_t slot) {
             const int k0 = s * BK;
@@ -272,11 +273,11 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
             const uint32_t at = my_ring + slot * SLOT;
 #pragma unroll
             for (int i = 0; i < NB; ++i)
-                dma16(rW, at + i * 1024, on && b_off[i] != OOB ? b_off[i] + kb2 : OOB);
+                dma16(rW, at + i * 1024, on ? b_off[i] + kb2 : OOB);
             const bool whole = on && k0 + 8 * a_c < p.K;
 #pragma unroll
             for (int i = 0; i < RB; ++i)
-                dma16(rX, at + B_SLOT + i * 1024, whole && a_off[i] != OOB ? a_off[i] + ka2 : OOB);
+                dma16(rX, at + B_SLOT + i * 1024, whole ? a_off[i] + ka2 : OOB);
         };
         f32x4_t acc[RB][NB];
 #pragma unroll

@@ -1,0 +1,276 @@
+// grouped_tile.hpp -- gfx950 device code of the grouped products with many
+// rows per group, where the matrix cores and the LDS bound them (see
+// grouped.hpp for what is computed and for few rows).
+//
+// A workgroup of eight waves (2 along rows, 4 along columns) takes a tile of
+// up to 256 positions of one group by 256 columns (for GLU 128 gate and the
+// same 128 up columns, so that a lane holds both).  K advances 32 per step
+// through four LDS stages filled by direct loads three steps ahead; the two
+// waves of a SIMD alternate, one reading fragments and asking for loads
+// while the other multiplies (the schedule of gc_kernel.hpp).  Gathered rows
+// cost nothing: every lane of a load has an address of its own.
+//
+// Tile heights 256, 192, 128 and 64 share one launch: a group's last tile is
+// as tall as its rows need.  A step moves 32 KB of fragments of W and 8 KB
+// per 32 rows through the LDS besides the loads' 16 KB + 2 KB per 32 rows, so
+// a 64-row tile costs about half of a 256-row one, not a quarter.
+//
+// The tiles of a group are numbered by bands of GROUP_M row tiles, columns
+// next, rows of the band last: the tiles in flight on one XCD share rows of X
+// and columns of W in its L2.  Each XCD has a queue, an equal piece of the
+// line of tiles, from which its workgroups draw tickets; a workgroup whose
+// queue is empty draws from the next, so the chip runs dry within one tile.
+#pragma once
+
+#include "grouped.hpp"
+
+namespace gc {
+
+constexpr int TK_QUEUES = 8, TK_GROUP_M = 6;
+// Counters of a launch, zero between launches: one ticket per queue (64 bytes
+// apart), and the workgroups that are through.
+constexpr int TK_TICKET_STRIDE = 16, TK_DONE = TK_QUEUES * TK_TICKET_STRIDE;
+
+struct TileAt {
+    int e, lo, hi, m0, nt;
+};
+
+// One tile of 32*FMT positions.
+template <int FMT, bool GLU>
+__device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, const TileAt &at, int wave,
+                                         int lane)
+{
+    constexpr int WMt = 16 * FMT, BMt = 2 * WMt;
+    const int wm = wave >> 2, wn = wave & 3;
+    const int fi = lane & 15, fg = lane >> 4;
+    const int F = GLU ? p.N / 2 : p.N;
+    const uint32_t N2 = (uint32_t)p.N * 2u;
+    const int KT = (p.K + BK - 1) / BK;
+    const u32x4_t rW = make_rsrc4(p.W + (size_t)at.e * p.K * p.N, (uint32_t)p.K * N2);
+    const u32x4_t rX = make_rsrc4(p.X, (uint32_t)p.T * (uint32_t)p.K * 2u);
+
+    // Loads, as in gc_kernel: instruction j of a wave fills rows 16 * (2 *
+    // wave + j) + lane / 4 of the A stage and rows 4 * wave + 2 * j + lane / 32
+    // of the B stage, with the stored chunks swizzled there.
+    const int a_c = (lane & 3) ^ ((lane >> 3) & 3);
+    uint32_t a_off[2], b_off[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int r = 16 * (2 * wave + j) + (lane >> 2), m = at.m0 + r;
+        int src = -1;
+        if (r < BMt && m >= at.lo && m < at.hi)
+            src = p.rows ? p.rows[m] : m;
+        a_off[j] = (unsigned)src < (unsigned)p.T
+                       ? ((uint32_t)src * (uint32_t)p.K + (uint32_t)(8 * a_c)) * 2u
+                       : OOB;
+        const int k = 4 * wave + 2 * j + (lane >> 5);
+        const int fk = (k & 3) | (((k >> 3) & 1) << 2);
+        const int slot = lane & 31;
+        const int c = 16 * ((slot >> 1) ^ fk) + 8 * (slot & 1);     // column in the tile
+        int n;
+        if (GLU) {
+            const int h = at.nt * (BN / 2) + (c & (BN / 2 - 1));
+            n = h >= F ? -1 : c < BN / 2 ? h : F + h;
+        } else {
+            n = at.nt * BN + c < p.N ? at.nt * BN + c : -1;
+        }
+        b_off[j] = n >= 0 ? ((uint32_t)k * (uint32_t)p.N + (uint32_t)n) * 2u : OOB;
+    }
+    auto stage = [&](int s) { return lds0 + (uint32_t)(s * (A_BYTES + B_BYTES)); };
+    // Loads of step kt; past the K loop the same number of empty ones.  (An
+    // offset of OOB plus a step's advance, below 2^31, is still out of range.)
+    auto load = [&](int kt, uint32_t st) {
+        const int k0 = kt * BK;
+        const uint32_t ka = (uint32_t)k0 * 2u, kb = (uint32_t)k0 * N2;
+        const uint32_t la = st + (uint32_t)(2 * wave * 1024);
+        const uint32_t lb = st + (uint32_t)(A_BYTES + 4 * wave * 512);
+        if (k0 + BK <= p.K) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                dma16(rX, la + j * 1024, a_off[j] + ka);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                dma16(rW, lb + j * 1024, b_off[j] + kb);
+        } else {
+            // (rows of W past K lie past its buffer)
+            const bool on = k0 + 8 * a_c < p.K;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                dma16(rX, la + j * 1024, on ? a_off[j] + ka : OOB);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                dma16(rW, lb + j * 1024, k0 < p.K ? b_off[j] + kb : OOB);
+        }
+    };
+    const uint32_t a_frag = (uint32_t)(wm * WMt * 64 + fi * 64 + ((fg ^ ((fi >> 1) & 3)) << 4));
+    const int fB = (fi >> 2) | ((fg & 1) << 2);
+    uint32_t b_frag[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+        // column block of the wave: for GLU blocks 0, 1 gate and 2, 3 up
+        const int q = GLU ? 8 * (j >> 1) + 2 * wn + (j & 1) : 4 * wn + j;
+        b_frag[j] = (uint32_t)(A_BYTES + (8 * fg + (fi >> 2)) * 512 + 8 * (fi & 3) + (q >> 3) * 256 +
+                               (((q & 7) ^ fB) * 32));
+    }
+    f32x4_t acc[FMT][FN];
+#pragma unroll
+    for (int i = 0; i < FMT; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+
+    load(0, stage(0));
+    load(1, stage(1));
+    load(2, stage(2));
+    const bool lag = wave >= 4;
+    wait_vmcnt<2 * DMA_PER_STEP>();
+    if (lag)
+        barrier_only();
+    auto step = [&](auto uc, int kt) {
+        constexpr int u = decltype(uc)::value;
+        const uint32_t cs = opaque(stage(u)), ns = stage((u + 3) & 3);
+        barrier_only();
+        bf16x8_t fa[FN], fb[FMT];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            bf16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                (lds_bf16x4_t *)lds_ptr<bf16x4_t>(cs + b_frag[j]));
+            bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                (lds_bf16x4_t *)lds_ptr<bf16x4_t>(cs + b_frag[j] + 4 * 512));
+            fa[j] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+#pragma unroll
+        for (int i = 0; i < FMT; ++i)
+            fb[i] = *lds_ptr<bf16x8_t>(cs + a_frag + i * 1024);
+        load(kt + 3, ns);
+        wait_vmcnt<2 * DMA_PER_STEP>();       // the wave's loads of step kt + 1 have landed
+        wait_lgkmcnt0();
+        barrier_only();
+#pragma unroll
+        for (int i = 0; i < FMT; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], fb[i], acc[i][j], 0, 0, 0);
+    };
+    int kt = 0;
+    for (; kt + 4 <= KT; kt += 4) {
+        step(std::integral_constant<int, 0>{}, kt);
+        step(std::integral_constant<int, 1>{}, kt + 1);
+        step(std::integral_constant<int, 2>{}, kt + 2);
+        step(std::integral_constant<int, 3>{}, kt + 3);
+    }
+    if (kt < KT)
+        step(std::integral_constant<int, 0>{}, kt);
+    if (kt + 1 < KT)
+        step(std::integral_constant<int, 1>{}, kt + 1);
+    if (kt + 2 < KT)
+        step(std::integral_constant<int, 2>{}, kt + 2);
+    if (!lag)
+        barrier_only();
+
+    // ---- epilogue: 16-byte stores of 8 columns per lane ----
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.S * (uint32_t)F * 2u);
+    const int ln = opaque_v(lane);
+    const int fi2 = ln & 15, fg2 = ln >> 4;
+    const int p8 = 8 * (fg2 >> 1) + 16 * (fg2 & 1);
+#pragma unroll
+    for (int i = 0; i < FMT; ++i) {
+        const int m = at.m0 + wm * WMt + 16 * i + fi2;
+        const bool row = m < at.hi;
+        if constexpr (GLU) {
+            const int n = at.nt * (BN / 2) + 32 * wn + p8;
+            const u32x4_t pk = pack_pair(silu_mul(acc[i][0], acc[i][2]), silu_mul(acc[i][1], acc[i][3]));
+            store16(ro, row && n < F ? ((uint32_t)m * (uint32_t)F + (uint32_t)n) * 2u : OOB, pk);
+        } else {
+#pragma unroll
+            for (int h = 0; h < FN / 2; ++h) {
+                const int n = at.nt * BN + 64 * wn + 32 * h + p8;
+                store16(ro, row && n < F ? ((uint32_t)m * (uint32_t)F + (uint32_t)n) * 2u : OOB,
+                        pack_pair(acc[i][2 * h], acc[i][2 * h + 1]));
+            }
+        }
+    }
+}
+
+template <bool GLU>
+__global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[STAGES * (A_BYTES + B_BYTES)];
+    __shared__ int first[GR_GROUPS + 1];
+    __shared__ int wsum[WAVES];
+    __shared__ int s_next;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = gridDim.x;
+    const int tiles = scan_tiles<NT>(p.offsets, p.E, p.S, p.E, BM, p.tiles_n, first, wsum);
+    // Queue x: tiles [x * tiles / 8, (x + 1) * tiles / 8).
+    int x = blockIdx.x & (TK_QUEUES - 1), tried = 0, mine = blockIdx.x / TK_QUEUES;
+    const int per_queue = (G + TK_QUEUES - 1) / TK_QUEUES;
+    auto begin = [&](int q) { return (int)((int64_t)tiles * q / TK_QUEUES); };
+    // Next tile for this workgroup, or -1 (thread 0 only).
+    auto draw = [&]() {
+        for (; tried < TK_QUEUES; ++tried, x = (x + 1) & (TK_QUEUES - 1), mine = 0) {
+            const int b = begin(x), n = begin(x + 1) - b;
+            int t;
+            if (p.count) {
+                t = (int)__hip_atomic_fetch_add(p.count + x * TK_TICKET_STRIDE, 1u, __ATOMIC_RELAXED,
+                                                __HIP_MEMORY_SCOPE_AGENT);
+            } else {                            // no workspace: equal shares
+                if (tried > 0)
+                    break;
+                t = mine;
+                mine += per_queue;
+            }
+            if (t < n)
+                return b + t;
+        }
+        return -1;
+    };
+    if (tid == 0)
+        s_next = draw();
+    const uint32_t lds0 = lds_addr(stages);
+    for (;;) {
+        __syncthreads();
+        const int t = __builtin_amdgcn_readfirstlane(s_next);
+        __syncthreads();
+        if (t < 0)
+            break;
+        if (tid == 0)
+            s_next = draw();
+        TileAt at;
+        at.e = __builtin_amdgcn_readfirstlane(find_group(first, p.E, t, lane));
+        group_range(p.offsets, p.E, p.S, at.e, at.lo, at.hi);
+        at.lo = __builtin_amdgcn_readfirstlane(at.lo);
+        at.hi = __builtin_amdgcn_readfirstlane(at.hi);
+        const int in = t - __builtin_amdgcn_readfirstlane(first[at.e]);
+        const int tiles_m = max((at.hi - at.lo + BM - 1) / BM, 1);
+        const int band = in / (TK_GROUP_M * p.tiles_n);
+        const int rest = in - band * TK_GROUP_M * p.tiles_n;
+        const int high = min(TK_GROUP_M, tiles_m - band * TK_GROUP_M);
+        at.nt = rest / max(high, 1);
+        at.m0 = at.lo + (band * TK_GROUP_M + rest - at.nt * high) * BM;
+        const int left = at.hi - at.m0;
+        if (left > 192)
+            run_tile<8, GLU>(p, lds0, at, wave, lane);
+        else if (left > 128)
+            run_tile<6, GLU>(p, lds0, at, wave, lane);
+        else if (left > 64)
+            run_tile<4, GLU>(p, lds0, at, wave, lane);
+        else
+            run_tile<2, GLU>(p, lds0, at, wave, lane);
+        wait_vmcnt<0>();                         // the stages are free for the next tile
+    }
+    // The last workgroup through leaves the counters at zero.
+    if (p.count && tid == 0) {
+        const uint32_t n = __hip_atomic_fetch_add(p.count + TK_DONE, 1u, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT);
+        if (n == (uint32_t)G - 1) {
+            for (int q = 0; q < TK_QUEUES; ++q)
+                __hip_atomic_store(p.count + q * TK_TICKET_STRIDE, 0u, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT);
+            __hip_atomic_store(p.count + TK_DONE, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+    }
+}
+
+}  // namespace gc

@@ -126,7 +126,8 @@ def test_group_rows(T, k, groups):
 
 # ---- grouped products ----
 
-SIZES = [[1], [0, 0, 5, 0], [16, 17, 0, 33, 1], [64, 65, 1, 63], [130, 0, 257], [7] * 30, [300, 520, 3]]
+SIZES = [[1], [0, 0, 5, 0], [16, 17, 0, 33, 1], [64, 65, 1, 63], [130, 0, 257], [7] * 30, [300, 520, 3],
+         [1700, 0, 200, 190, 60, 129]]
 
 
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: "x".join(map(str, s[:5])))
