@@ -60,8 +60,9 @@ extern "C" {
 #define GC_ACT_NONE 0
 #define GC_ACT_SILU_GLU 1
 
-/* Bytes of workspace that every call here except lora_add can be given on
- * the current device (about 16 MiB on MI355X); negative on a HIP error. */
+/* Bytes of workspace that every call here can be given on the current device
+ * (about 16 MiB on MI355X; lora_add of many rows needs more); negative on a
+ * HIP error. */
 int64_t gemm_coll_grouped_workspace_bytes(void);
 
 /*
@@ -127,7 +128,7 @@ int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, con
  *   out[m] = bf16( base[m] + (scale[a] * X[m] . down[a]) . up[a] )
  * with X [M][K], base and out [M][N], down [G][K][r], up [G][r][N],
  * scale float [G], offsets and rows [M] a grouping of the M rows by adapter.
- * The middle activations are kept as a sum of two bf16 (16 bits of
+ * The middle activations are fp32 sums, multiplied as two bf16 (16 bits of
  * mantissa).  Rows in no group: out is base (base == out: untouched).
  * r <= 128, a multiple of 8; G <= 1023.  Needs
  * gemm_coll_lora_workspace_bytes(M, r) bytes of workspace.

@@ -47,10 +47,10 @@ bool good4(const void *p) { return p && aligned(p, 4); }
 // sentinel at 2^31.
 bool fits(int64_t rows, int64_t cols) { return cols == 0 || rows < ((int64_t)1 << 30) / cols; }
 
-// Workspace: arrival counters (one per workgroup of the streaming kernel),
-// then partial tiles, two of at most kPartBytes per workgroup.  The many-block
-// grouping keeps its counts where the partial tiles are, and lora_add its
-// middle activations behind them.
+// Workspace: counters (4 KiB, zero between launches), then partial tiles of
+// the streaming kernel, two of at most kPartBytes per workgroup.  The
+// many-block grouping keeps its counts where the partial tiles are, and
+// lora_add its middle sums.
 constexpr int64_t kCountBytes = 4096;
 constexpr int64_t kPartBytes = 32768;
 constexpr int kMaxWorkers = (int)(kCountBytes / 4);
@@ -133,6 +133,30 @@ void launch_stream_rows(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hip
         launch_stream<NB, 4, 3, EPI>(a, cus, st);
 }
 
+// Middle sums of the adapters: tiles of 16, 32 or 64 rows, K cut into so many
+// pieces that every CU has one (tile, piece), but none shorter than 8 steps.
+template <int NB, int RB, int D>
+void launch_sums_rows(gc::GroupedArgs &a, int cus, hipStream_t st)
+{
+    const int bm = 16 * RB, kt = (a.K + gc::BK - 1) / gc::BK;
+    const int tiles = (int)std::min<int64_t>(a.S, (int64_t)(a.S + bm - 1) / bm + a.E);
+    a.tiles_n = 1;
+    a.splits = std::max(1, std::min({16, cus / tiles, kt / 8}));
+    const int grid = (int)std::min<int64_t>((int64_t)tiles * a.splits, 4 * cus);
+    hipLaunchKernelGGL((gc::stream_kernel<NB, RB, D, gc::EPI_SUMS>), dim3(grid), dim3(gc::ST_THREADS), 0, st, a);
+}
+
+template <int NB>
+void launch_sums(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hipStream_t st)
+{
+    if (rows_per_group <= 16)
+        launch_sums_rows<NB, 1, 4>(a, cus, st);
+    else if (rows_per_group <= 32)
+        launch_sums_rows<NB, 2, 3>(a, cus, st);
+    else
+        launch_sums_rows<NB, 4, 3>(a, cus, st);
+}
+
 template <bool GLU>
 void launch_tiles(gc::GroupedArgs &a, int cus, hipStream_t st)
 {
@@ -169,7 +193,7 @@ int64_t gemm_coll_lora_workspace_bytes(int64_t M, int r)
         return GC_EINVAL;
     int cus = 0;
     const int err = cu_count(cus);
-    return err ? err : base_bytes(cus) + 2 * (M * r * 2 + 255) / 256 * 256;
+    return err ? err : std::max(base_bytes(cus), kCountBytes + M * r * 4);
 }
 
 int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int64_t T, int E, int k,
@@ -348,40 +372,35 @@ int gemm_coll_lora_add(const gc_bf16 *base, const gc_bf16 *X, const gc_bf16 *dow
     int cus = 0;
     if (int err = cu_count(cus))
         return err;
-    const int64_t hb = (M * r * 2 + 255) / 256 * 256;
-    if (!good16(workspace) || workspace_bytes < (uint64_t)(base_bytes(cus) + 2 * hb))
+    if (!good16(workspace) || workspace_bytes < (uint64_t)std::max(base_bytes(cus), kCountBytes + M * r * 4))
         return GC_EINVAL;
-    char *ws = (char *)workspace;
     const hipStream_t st = (hipStream_t)stream;
     gc::GroupedArgs a = {};
     a.X = X;
     a.W = down;
     a.offsets = offsets;
     a.rows = rows;
-    a.scale = scale;
-    a.out = (uint16_t *)(ws + base_bytes(cus));
-    a.out_lo = (uint16_t *)(ws + base_bytes(cus) + hb);
+    a.sums = (float *)((char *)workspace + kCountBytes);
     a.T = (int)M;
     a.S = (int)M;
     a.K = (int)K;
     a.N = r;
     a.E = G;
-    a.count = (uint32_t *)ws;
-    a.part = (float *)(ws + kCountBytes);
     const int64_t avg = (M + G - 1) / G;
     if (r <= 16)
-        launch_stream_rows<1, gc::EPI_SPLIT>(a, avg, cus, st);
+        launch_sums<1>(a, avg, cus, st);
     else if (r <= 32)
-        launch_stream_rows<2, gc::EPI_SPLIT>(a, avg, cus, st);
+        launch_sums<2>(a, avg, cus, st);
     else if (r <= 64)
-        launch_stream_rows<4, gc::EPI_SPLIT>(a, avg, cus, st);
+        launch_sums<4>(a, avg, cus, st);
     else
-        launch_stream_rows<8, gc::EPI_SPLIT>(a, avg, cus, st);
+        launch_sums<8>(a, avg, cus, st);
     gc::ExpandArgs x = {};
     x.base = base;
     x.out = out;
-    x.h = a.out;
-    x.h_lo = a.out_lo;
+    x.sums = a.sums;
+    x.scale = scale;
+    x.splits = a.splits;
     x.up = up;
     x.offsets = offsets;
     x.rows = rows;
@@ -390,12 +409,17 @@ int gemm_coll_lora_add(const gc_bf16 *base, const gc_bf16 *X, const gc_bf16 *dow
     x.r = r;
     x.E = G;
     x.copy = out != base;
-    x.tiles_n = (int)((N + gc::EX_COLS - 1) / gc::EX_COLS);
-    const int bm = avg >= 32 ? 64 : 16;
-    const int64_t tiles = std::min<int64_t>(M, (M + bm - 1) / bm + G) * x.tiles_n;
-    const int grid = (int)std::min<int64_t>(tiles, (int64_t)cus * 4);
-    if (bm == 64)
-        launch_expand<4>(x, grid, st);
+    // Spans: as many workgroups as the CUs hold at once (three each), for every
+    // span adds up its rows' H again.
+    const int bm = avg >= 24 ? 32 : 16;
+    const int64_t tiles_n = (N + gc::EX_COLS - 1) / gc::EX_COLS;
+    const int64_t tiles_m = std::min<int64_t>(M, (M + bm - 1) / bm + G);
+    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, 3 * cus / tiles_m));
+    x.span = (int)((tiles_n + want - 1) / want);
+    x.spans = (int)((tiles_n + x.span - 1) / x.span);
+    const int grid = (int)std::min<int64_t>(tiles_m * x.spans, (int64_t)cus * 8);
+    if (bm == 32)
+        launch_expand<2>(x, grid, st);
     else
         launch_expand<1>(x, grid, st);
     return launched();

@@ -5,9 +5,8 @@
 // with one of three ends:
 //   PLAIN  out[i] = bf16(y[i])
 //   GLU    out[i] = bf16(silu(y[i][:N/2]) * y[i][N/2:])
-//   SPLIT  out[i] + out_lo[i] = scale[e] * y[i] as two bf16 (the rounded value
-//          and the rounded rest: 16 bits of mantissa instead of 8), the
-//          adapters' middle activations
+//   SUMS   fp32 y[i] over each of `splits` equal pieces of K, the adapters'
+//          middle activations, which their reader adds up in the order of K
 //
 // stream_kernel: few rows per group, so the weights' bytes bound it.  A tile
 // is 16*RB positions of one group by 16*NB columns of W[e]; the four waves of
@@ -16,7 +15,7 @@
 // (D - 1) * 4 steps of weights are in flight per CU all the time.  The waves'
 // sums are added through LDS at the end of the tile.
 //
-// Work is dealt out evenly whatever the groups' sizes: the K-steps of all
+// PLAIN and GLU: work is dealt out evenly whatever the groups' sizes: the K-steps of all
 // tiles, counted in quads of 4 (one per wave), form one line, and workgroup w
 // takes the w-th of equal pieces of it.  A tile whose K range is cut by a
 // piece's end is finished by the last of its workgroups to arrive, which adds
@@ -28,7 +27,7 @@
 
 namespace gc {
 
-enum Epilogue { EPI_PLAIN = 0, EPI_GLU = 1, EPI_SPLIT = 2 };
+enum Epilogue { EPI_PLAIN = 0, EPI_GLU = 1, EPI_SUMS = 2 };
 
 constexpr int GR_GROUPS = 1024;           // groups at most
 
@@ -37,9 +36,9 @@ struct GroupedArgs {
     const uint16_t *W;         // [E][K][N]
     const int32_t *offsets;    // [E + 1]
     const int32_t *rows;       // [S] or null
-    const float *scale;        // SPLIT: [E]
-    uint16_t *out;             // PLAIN [S][N], GLU [S][N/2], SPLIT [S][N]
-    uint16_t *out_lo;          // SPLIT [S][N]
+    uint16_t *out;             // PLAIN [S][N], GLU [S][N/2]
+    float *sums;               // SUMS [splits][S][N]
+    int splits;
     int T, S, K, N, E;
     int tiles_n;               // column tiles
     int min_quads;             // smallest piece of a tile that a workgroup takes
@@ -189,13 +188,21 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
     line.per_tile = max((KT + ST_WAVES - 1) / ST_WAVES, 1);
     line.quads = (int64_t)tiles * line.per_tile;
     line.least = p.min_quads;
-    line.pieces = (int)min((int64_t)min(G, p.part_slots / 2),
-                           max((int64_t)1, line.quads / max(p.min_quads, 1)));
-    if ((int)blockIdx.x >= line.pieces)
-        return;
-    const int v = xcd_remap(blockIdx.x, line.pieces);
-    int64_t q = line.bound(v);
-    const int64_t q_end = line.bound(v + 1);
+    line.pieces = G;
+    int64_t q, q_end;
+    int v = blockIdx.x;
+    if constexpr (EPI == EPI_SUMS) {
+        q = v;                                           // units: (tile, piece of K)
+        q_end = (int64_t)tiles * p.splits;
+    } else {
+        line.pieces = (int)min((int64_t)min(G, p.part_slots / 2),
+                               max((int64_t)1, line.quads / max(p.min_quads, 1)));
+        if (v >= line.pieces)
+            return;
+        v = xcd_remap(v, line.pieces);
+        q = line.bound(v);
+        q_end = line.bound(v + 1);
+    }
 
     // Loads of W: lane = row lane / (64 / RPI) of the instruction's RPI rows,
     // 16-byte slot lane % (BN / 8) of the row.  The 32-byte chunk c of row k
@@ -220,10 +227,21 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
     const uint32_t my_ring = lds_addr(ring) + (uint32_t)(wave * D * SLOT);
 
     while (q < q_end) {
-        const int t = (int)(q / line.per_tile);
-        const int ka = (int)(q - (int64_t)t * line.per_tile);
-        const int kb = (int)min((int64_t)line.per_tile, ka + (q_end - q));
-        q += kb - ka;
+        int t, ka, kb;
+        [[maybe_unused]] int piece = 0;
+        if constexpr (EPI == EPI_SUMS) {
+            t = (int)(q / p.splits);
+            piece = (int)(q - (int64_t)t * p.splits);
+            const int len = (line.per_tile + p.splits - 1) / p.splits;
+            ka = min(piece * len, line.per_tile);
+            kb = min(ka + len, line.per_tile);
+            q += G;
+        } else {
+            t = (int)(q / line.per_tile);
+            ka = (int)(q - (int64_t)t * line.per_tile);
+            kb = (int)min((int64_t)line.per_tile, ka + (q_end - q));
+            q += kb - ka;
+        }
         const int e = __builtin_amdgcn_readfirstlane(find_group(first, p.E, t, lane));
         int lo, hi;
         group_range(p.offsets, p.E, p.S, e, lo, hi);
@@ -335,7 +353,7 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
         };
 
         // ---- a cut tile: hand the partial over, the last to arrive goes on ----
-        const bool cut = ka > 0 || kb < line.per_tile;
+        const bool cut = EPI != EPI_SUMS && (ka > 0 || kb < line.per_tile);
         int w_first = v, w_last = v;
         const __amdgpu_buffer_rsrc_t rp =
             make_rsrc(p.part, (uint32_t)p.part_slots * (uint32_t)(RB * NB * 1024));
@@ -383,18 +401,13 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
 
         // ---- epilogue ----
         const int p8 = 8 * (fg >> 1) + 16 * (fg & 1);    // first column of a lane in a pair
-        if constexpr (EPI == EPI_SPLIT) {
-            const float sc = p.scale[e];
+        if constexpr (EPI == EPI_SUMS) {
             for (int b = wave; b < RB * NB; b += ST_WAVES) {
                 const int i = b / NB, j = b - i * NB;
-                const f32x4_t x = sc * final_sum(b);
                 const int m = m0 + 16 * i + fi, n = nt * BN + 16 * j + 4 * fg;
-                const u32x2_t h = pack_bf16x4(x);
-                const u32x2_t r = pack_bf16x4(x - unpack_bf16x4(h));
-                if (m < hi && n < p.N) {
-                    *(u32x2_t *)(p.out + (size_t)m * p.N + n) = h;
-                    *(u32x2_t *)(p.out_lo + (size_t)m * p.N + n) = r;
-                }
+                const f32x4_t x = block_sum(b);
+                if (m < hi && n < p.N)
+                    *(f32x4_t *)(p.sums + ((size_t)piece * p.S + m) * p.N + n) = x;
             }
         } else {
             constexpr int PAIRS = EPI == EPI_GLU ? NB / 4 : NB / 2;

@@ -123,115 +123,134 @@ __device__ __forceinline__ float soft_term(float x, float high)
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// Routes one token in one wave.  Lane j < k returns with the j-th choice's
-// expert (-1: none) in `id` and its weight in `w`.
-template <int VPL, bool BF16>
-__device__ __forceinline__ void route_token(const RouteArgs &p, int t, int lane, int &id, float &w)
+// Tokens that a wave routes side by side: a round is a chain of some twenty
+// dependent steps (the maximum over the wave, the ballot, the removal), which
+// one token alone would wait through.
+template <int VPL>
+constexpr int ROUTE_TOK = VPL <= 4 ? 4 : VPL == 8 ? 2 : 1;
+
+// Routes tokens t, t + RT_WAVES, ... (those below t1) in one wave.  Lane j < k
+// returns with the j-th choice's expert (-1: none) in id[] and its weight in w[].
+template <int VPL, bool BF16, int TOK>
+__device__ __forceinline__ void route_tokens(const RouteArgs &p, int t, int t1, int lane, int (&id)[TOK],
+                                             float (&w)[TOK])
 {
     const int e0 = lane * VPL;
-    float x[VPL];
-    if constexpr (BF16) {
-        const uint16_t *row = (const uint16_t *)p.logits + (int64_t)t * p.stride;
-        uint16_t b[VPL];
-        if (p.vec && e0 < p.E) {
-            __builtin_memcpy(b, __builtin_assume_aligned(row + e0, VPL * 2 < 16 ? VPL * 2 : 16), sizeof b);
-        } else {
+    const bool soft = p.score == SCORE_SOFTMAX;
+    float x[TOK][VPL], high[TOK], val[TOK];
+    uint32_t key[TOK][VPL];
+#pragma unroll
+    for (int q = 0; q < TOK; ++q) {
+        const int tq = t + q * RT_WAVES;
+        const bool live = tq < t1;
+        if constexpr (BF16) {
+            const uint16_t *row = (const uint16_t *)p.logits + (int64_t)(live ? tq : t) * p.stride;
+            uint16_t b[VPL];
+            if (p.vec && e0 < p.E) {
+                __builtin_memcpy(b, __builtin_assume_aligned(row + e0, VPL * 2 < 16 ? VPL * 2 : 16), sizeof b);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    b[i] = e0 + i < p.E ? row[e0 + i] : (uint16_t)0xFF80;
+            }
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                b[i] = e0 + i < p.E ? row[e0 + i] : (uint16_t)0xFF80;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            x[i] = __uint_as_float((uint32_t)b[i] << 16);
-    } else {
-        const float *row = (const float *)p.logits + (int64_t)t * p.stride;
-        if (p.vec && e0 < p.E) {
-            __builtin_memcpy(x, __builtin_assume_aligned(row + e0, VPL * 4 < 16 ? VPL * 4 : 16), sizeof x);
+                x[q][i] = __uint_as_float((uint32_t)b[i] << 16);
         } else {
+            const float *row = (const float *)p.logits + (int64_t)(live ? tq : t) * p.stride;
+            if (p.vec && e0 < p.E) {
+                __builtin_memcpy(x[q], __builtin_assume_aligned(row + e0, VPL * 4 < 16 ? VPL * 4 : 16),
+                                 sizeof x[q]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                x[i] = e0 + i < p.E ? row[e0 + i] : -__builtin_huge_valf();
+                for (int i = 0; i < VPL; ++i)
+                    x[q][i] = e0 + i < p.E ? row[e0 + i] : -__builtin_huge_valf();
+            }
         }
     }
-    uint32_t key[VPL];
-    float high = 0.f;
-    const bool soft = p.score == SCORE_SOFTMAX;
-    if (p.bias) {
-        // scores first, for their sum with the bias is what is compared
-        if (soft) {
-            uint32_t m = 0;
+#pragma unroll
+    for (int q = 0; q < TOK; ++q) {
+        high[q] = val[q] = 0.f;
+        id[q] = -1;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            key[q][i] = e0 + i < p.E ? order_key(x[q][i]) : 0u;
+        if (p.bias) {
+            // scores first, for their sum with the bias is what is compared
+            float total = 1.f;
+            if (soft) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    m = max(m, key[q][i]);
+                high[q] = key_value(wave_max_u32(m));
+                float part = 0.f;
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    part += key[q][i] > KEY_NEG_INF ? soft_term(x[q][i], high[q]) : 0.f;
+                total = wave_sum(part);
+            }
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const bool any = key[q][i] > KEY_NEG_INF;
+                x[q][i] = !any ? 0.f : soft ? soft_term(x[q][i], high[q]) / total : sigmoid(x[q][i]);
+                key[q][i] = any ? order_key(x[q][i] + p.bias[e0 + i]) : 0u;
+            }
+        }
+    }
+    for (int j = 0; j < p.k; ++j) {
+        uint32_t m[TOK], top[TOK];
+        int at[TOK];
+        float s[TOK];
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) {
+            m[q] = key[q][0];
+            at[q] = 0;
+            s[q] = x[q][0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i)
+                if (key[q][i] > m[q]) {
+                    m[q] = key[q][i];
+                    at[q] = i;
+                    s[q] = x[q][i];
+                }
+        }
+#pragma unroll
+        for (int q = 0; q < TOK; ++q)
+            top[q] = wave_max_u32(m[q]);
+#pragma unroll
+        for (int q = 0; q < TOK; ++q) {
+            // (with nothing left, the lane found is given no choice below)
+            const int wl = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m[q] == top[q]));
+            const int won = wl * VPL + __builtin_amdgcn_readlane(at[q], wl);
+            const float ws = p.bias ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s[q]), wl))
+                                    : key_value(top[q]);
+            const bool any = top[q] > KEY_NEG_INF;
+            if (j == 0 && !p.bias)
+                high[q] = ws;
+            id[q] = any && lane == j ? won : id[q];
+            val[q] = any && lane == j ? ws : val[q];
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                m = max(m, e0 + i < p.E ? order_key(x[i]) : 0u);
-            high = key_value(wave_max_u32(m));
+                key[q][i] = lane == wl && i == at[q] ? 0u : key[q][i];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < TOK; ++q) {
+        w[q] = id[q] < 0 ? 0.f : p.bias ? val[q] : soft ? soft_term(val[q], high[q]) : sigmoid(val[q]);
+        if (p.renorm) {
+            const float total = wave_sum(w[q]);
+            w[q] = total > 0.f ? w[q] / total : 0.f;
+        } else if (soft && !p.bias) {
             float part = 0.f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                part += e0 + i < p.E && order_key(x[i]) > KEY_NEG_INF ? soft_term(x[i], high) : 0.f;
+                part += e0 + i < p.E && order_key(x[q][i]) > KEY_NEG_INF ? soft_term(x[q][i], high[q]) : 0.f;
             const float total = wave_sum(part);
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool any = e0 + i < p.E && order_key(x[i]) > KEY_NEG_INF;
-                x[i] = any ? soft_term(x[i], high) / total : 0.f;
-                key[i] = any ? order_key(x[i] + p.bias[e0 + i]) : 0u;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool any = e0 + i < p.E && order_key(x[i]) > KEY_NEG_INF;
-                x[i] = any ? sigmoid(x[i]) : 0.f;
-                key[i] = any ? order_key(x[i] + p.bias[e0 + i]) : 0u;
-            }
+            w[q] = total > 0.f ? w[q] / total : 0.f;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            key[i] = e0 + i < p.E ? order_key(x[i]) : 0u;
+        w[q] *= p.scale;
     }
-    id = -1;
-    float val = 0.f;
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t m = key[0];
-        int at = 0;
-        float s = x[0];
-#pragma unroll
-        for (int i = 1; i < VPL; ++i)
-            if (key[i] > m) {
-                m = key[i];
-                at = i;
-                s = x[i];
-            }
-        const uint32_t top = wave_max_u32(m);
-        if (top <= KEY_NEG_INF)
-            break;
-        const int wl = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m == top));
-        const int won = wl * VPL + __builtin_amdgcn_readlane(at, wl);
-        const float ws =
-            p.bias ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), wl)) : key_value(top);
-        if (j == 0 && !p.bias)
-            high = ws;
-        if (lane == j) {
-            id = won;
-            val = ws;
-        }
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane == wl && i == at)
-                key[i] = 0u;
-    }
-    w = id < 0 ? 0.f : p.bias ? val : soft ? soft_term(val, high) : sigmoid(val);
-    if (p.renorm) {
-        const float total = wave_sum(w);
-        w = total > 0.f ? w / total : 0.f;
-    } else if (soft && !p.bias) {
-        float part = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            part += e0 + i < p.E && order_key(x[i]) > KEY_NEG_INF ? soft_term(x[i], high) : 0.f;
-        const float total = wave_sum(part);
-        w = total > 0.f ? w / total : 0.f;
-    }
-    w *= p.scale;
 }
 
 // LDS of the grouping.
@@ -242,13 +261,11 @@ struct GroupLds {
     int wave_sum[RT_WAVES];
 };
 
-// Exclusive prefix sum of l.total[0 .. groups) over the workgroup; returns it
-// for group threadIdx.x (any value past the groups), and the whole sum to
-// every thread.
-__device__ __forceinline__ int group_scan(GroupLds &l, int groups, int &all)
+// Exclusive prefix sum of v over threads 0 .. RT_THREADS - 1, and the whole
+// sum (one barrier).
+__device__ __forceinline__ int block_scan(GroupLds &l, int v, int &all)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int v = tid < groups ? l.total[tid] : 0;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int inc = wave_scan(v);
     if (lane == 63)
         l.wave_sum[wave] = inc;
@@ -263,50 +280,46 @@ __device__ __forceinline__ int group_scan(GroupLds &l, int groups, int &all)
     return before + inc - v;
 }
 
-// Places n items of consecutive flat numbers first, first + 1, ...: item i of
-// group get(i) (`groups` for none) goes to the next position of its group,
-// in the order of the items.  l.base holds each group's next position.
-template <class F>
-__device__ __forceinline__ void place_items(GroupLds &l, F &&get, int n, int first, int k, int groups,
-                                            int32_t *rows, int32_t *slots)
+__device__ __forceinline__ void clear_wave_at(GroupLds &l, int waves, int groups)
 {
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    for (int w = 0; w < waves; ++w)
+        for (int e = threadIdx.x; e <= groups; e += RT_THREADS)
+            l.wave_at[w][e] = 0;
+}
+
+// Rank of the lane's item among the earlier items of its wave in the same
+// group g, the group's count in the wave written to l.wave_at (cleared
+// before): one ballot per bit of the group number.
+__device__ __forceinline__ int rank_in_wave(GroupLds &l, bool live, int g, int groups)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int bits = 32 - __builtin_clz(groups);       // groups itself is a value
-    for (int i0 = 0; i0 < n; i0 += RT_THREADS) {
-        for (int w = 0; w < RT_WAVES; ++w)
-            for (int e = tid; e <= groups; e += RT_THREADS)
-                l.wave_at[w][e] = 0;
-        __syncthreads();
-        const int i = i0 + tid;
-        const bool live = i < n;
-        const int g = live ? get(i) : 0;
-        uint64_t same = __builtin_amdgcn_ballot_w64(live);
-        for (int b = 0; b < bits; ++b) {
-            const uint64_t on = __builtin_amdgcn_ballot_w64((g >> b) & 1);
-            same &= (g >> b) & 1 ? on : ~on;
-        }
-        const int rank = __builtin_popcountll(same & ((1ull << lane) - 1ull));
-        if (live && rank == 0)
-            l.wave_at[wave][g] = __builtin_popcountll(same);
-        __syncthreads();
-        for (int e = tid; e <= groups; e += RT_THREADS) {
-            int at = l.base[e];
-            for (int w = 0; w < RT_WAVES; ++w) {
-                const int c = l.wave_at[w][e];
-                l.wave_at[w][e] = at;
-                at += c;
-            }
-            l.base[e] = at;
-        }
-        __syncthreads();
-        if (live) {
-            const int pos = l.wave_at[wave][g] + rank;
-            const int flat = first + i;
-            rows[pos] = (int)((unsigned)flat / (unsigned)k);
-            slots[flat] = g == groups ? -1 : pos;
-        }
-        __syncthreads();
+    uint64_t same = __builtin_amdgcn_ballot_w64(live);
+    for (int b = 0; b < bits; ++b) {
+        const uint64_t on = __builtin_amdgcn_ballot_w64((g >> b) & 1);
+        same &= (g >> b) & 1 ? on : ~on;
     }
+    const int rank = __builtin_popcountll(same & ((1ull << lane) - 1ull));
+    if (live && rank == 0)
+        l.wave_at[wave][g] = __builtin_popcountll(same);
+    return rank;
+}
+
+// Counts of group e in the waves to positions from `at` on; returns the next.
+__device__ __forceinline__ int counts_to_positions(GroupLds &l, int waves, int e, int at)
+{
+    for (int w = 0; w < waves; ++w) {
+        const int c = l.wave_at[w][e];
+        l.wave_at[w][e] = at;
+        at += c;
+    }
+    return at;
+}
+
+__device__ __forceinline__ void place(const RouteArgs &p, int flat, int g, int pos)
+{
+    p.rows[pos] = (int)((unsigned)flat / (unsigned)p.k);
+    p.slots[flat] = g == p.E ? -1 : pos;
 }
 
 // Group of an id from outside: ids past the groups are in none.
@@ -316,10 +329,12 @@ __device__ __forceinline__ int group_of(int id, int groups)
 }
 
 // Routes the tokens of this block (VPL > 0) or reads their ids (VPL == 0),
-// then: ONE (a single workgroup) groups them, else counts them per group.
+// then: ONE (a single workgroup, at most ROUTE_ONE_ITEMS items) groups them,
+// else counts them per group.
 template <int VPL, bool BF16, bool ONE>
 __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
 {
+    static_assert(ROUTE_ONE_ITEMS <= RT_THREADS, "one item per thread");
     __shared__ GroupLds l;
     __shared__ int s_id[ONE ? ROUTE_ONE_ITEMS : 1];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -327,52 +342,72 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
     const int t0 = ONE ? 0 : blockIdx.x * p.block_tokens;
     const int t1 = ONE ? p.T : min(p.T, t0 + p.block_tokens);
     const bool group = p.offsets != nullptr;
+    const int n = p.T * p.k, waves = (n + 63) / 64;      // (ONE)
     if (group) {
-        for (int e = tid; e <= p.E; e += RT_THREADS)
-            l.total[e] = 0;
-        __syncthreads();
+        if (ONE) {
+            clear_wave_at(l, waves, p.E);
+        } else {
+            for (int e = tid; e <= p.E; e += RT_THREADS)
+                l.total[e] = 0;
+            __syncthreads();
+        }
     }
     if constexpr (VPL > 0) {
-        for (int t = t0 + wave; t < t1; t += RT_WAVES) {
-            int id;
-            float w;
-            route_token<VPL, BF16>(p, t, lane, id, w);
-            if (lane < p.k) {
-                const int flat = t * p.k + lane;
-                p.ids[flat] = id;
-                p.weights[flat] = w;
-                if (group) {
-                    const int g = id < 0 ? p.E : id;
-                    atomicAdd(&l.total[g], 1);
-                    if (ONE)
-                        s_id[flat] = g;
+        constexpr int TOK = ROUTE_TOK<VPL>;
+        for (int t = t0 + wave; t < t1; t += RT_WAVES * TOK) {
+            int id[TOK];
+            float w[TOK];
+            route_tokens<VPL, BF16, TOK>(p, t, t1, lane, id, w);
+#pragma unroll
+            for (int q = 0; q < TOK; ++q) {
+                const int tq = t + q * RT_WAVES;
+                if (lane < p.k && tq < t1) {
+                    const int flat = tq * p.k + lane;
+                    p.ids[flat] = id[q];
+                    p.weights[flat] = w[q];
+                    if (group) {
+                        const int g = id[q] < 0 ? p.E : id[q];
+                        if (ONE)
+                            s_id[flat] = g;
+                        else
+                            atomicAdd(&l.total[g], 1);
+                    }
                 }
             }
         }
     } else {
         for (int i = t0 * p.k + tid; i < t1 * p.k; i += RT_THREADS) {
             const int g = group_of(p.ids[i], p.E);
-            atomicAdd(&l.total[g], 1);
             if (ONE)
                 s_id[i] = g;
+            else
+                atomicAdd(&l.total[g], 1);
         }
     }
     if (!group)
         return;
     __syncthreads();
     if constexpr (ONE) {
-        int all;
-        const int at = group_scan(l, p.E, all);
+        const bool live = tid < n;
+        const int g = live ? s_id[tid] : 0;
+        const int rank = rank_in_wave(l, live, g, p.E);
+        __syncthreads();
+        int sum = 0, all;
+        if (tid < p.E)
+            for (int w = 0; w < waves; ++w)
+                sum += l.wave_at[w][tid];
+        const int at = block_scan(l, sum, all);
         if (tid < p.E) {
-            l.base[tid] = at;
+            counts_to_positions(l, waves, tid, at);
             p.offsets[tid] = at;
         }
-        if (tid == 0) {
-            l.base[p.E] = all;
+        if (tid == RT_THREADS - 1) {
+            counts_to_positions(l, waves, p.E, all);
             p.offsets[p.E] = all;
         }
         __syncthreads();
-        place_items(l, [&](int i) { return s_id[i]; }, p.T * p.k, 0, p.k, p.E, p.rows, p.slots);
+        if (live)
+            place(p, tid, g, l.wave_at[wave][g] + rank);
     } else {
         for (int e = tid; e < p.cstride; e += RT_THREADS)
             p.counts[(int64_t)blockIdx.x * p.cstride + e] = e <= p.E ? (uint16_t)l.total[e] : (uint16_t)0;
@@ -383,7 +418,7 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
 __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
 {
     __shared__ GroupLds l;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, wave = tid >> 6;
     const int blocks = gridDim.x, b = blockIdx.x;
     for (int e = tid; e < p.cstride; e += RT_THREADS) {
         l.base[e] = 0;
@@ -391,7 +426,9 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
     }
     __syncthreads();
     // Counts of the blocks before this one (base) and of all (total): a
-    // thread adds 8 neighbouring groups over every per_pass-th block.
+    // thread adds 8 neighbouring groups over every per_pass-th block.  In the
+    // LDS, group 8 c + i is kept at i * lanes + c, so that the lanes of an
+    // addition, whose c differ, fall into different banks.
     const int lanes = p.cstride / 8, per_pass = RT_THREADS / lanes;
     const int r0 = tid / lanes, c = tid - r0 * lanes;
     if (r0 < per_pass) {
@@ -408,28 +445,41 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            atomicAdd(&l.total[8 * c + i], tot[i]);
-            atomicAdd(&l.base[8 * c + i], pre[i]);
+            atomicAdd(&l.total[i * lanes + c], tot[i]);
+            atomicAdd(&l.base[i * lanes + c], pre[i]);
         }
     }
     __syncthreads();
+    auto kept = [&](int e) { return (e & 7) * lanes + (e >> 3); };
     int all;
-    const int at = group_scan(l, p.E, all);
+    const int at = block_scan(l, tid < p.E ? l.total[kept(tid)] : 0, all);
     if (tid < p.E) {
-        l.base[tid] += at;
+        l.base[kept(tid)] += at;
         if (b == 0)
             p.offsets[tid] = at;
     }
     if (tid == 0) {
-        l.base[p.E] += all;
+        l.base[kept(p.E)] += all;
         if (b == 0)
             p.offsets[p.E] = all;
     }
-    __syncthreads();
     const int first = b * p.block_tokens * p.k;
     const int n = (min(p.T, (b + 1) * p.block_tokens) - b * p.block_tokens) * p.k;
-    place_items(l, [&](int i) { return group_of(p.ids[first + i], p.E); }, n, first, p.k, p.E, p.rows,
-                p.slots);
+    for (int i0 = 0; i0 < n; i0 += RT_THREADS) {
+        const int waves = min(RT_WAVES, (n - i0 + 63) / 64);
+        clear_wave_at(l, waves, p.E);
+        const bool live = i0 + tid < n;
+        const int g = live ? group_of(p.ids[first + i0 + tid], p.E) : 0;
+        __syncthreads();
+        const int rank = rank_in_wave(l, live, g, p.E);
+        __syncthreads();
+        for (int e = tid; e <= p.E; e += RT_THREADS)
+            l.base[kept(e)] = counts_to_positions(l, waves, e, l.base[kept(e)]);
+        __syncthreads();
+        if (live)
+            place(p, first + i0 + tid, g, l.wave_at[wave][g] + rank);
+        __syncthreads();
+    }
 }
 
 }  // namespace gc
