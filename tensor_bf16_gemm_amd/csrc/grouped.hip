@@ -60,31 +60,49 @@ int64_t base_bytes(int cus) { return kCountBytes + 2 * kPartBytes * workers(cus)
 
 int launched() { return hipGetLastError() == hipSuccess ? GC_OK : GC_EIO; }
 
+// Lanes per token and experts per lane: rows of 16 lanes up to 256 experts,
+// whole waves beyond.
+int route_lanes(int E) { return E <= 256 ? 16 : 64; }
+int route_values(int E)
+{
+    int v = 1;
+    while (v * route_lanes(E) < E)
+        v *= 2;
+    return v;
+}
+
 template <bool BF16, bool ONE>
-void launch_route(const gc::RouteArgs &a, int vpl, int blocks, hipStream_t st)
+void launch_route(const gc::RouteArgs &a, int blocks, hipStream_t st)
 {
     const dim3 g(blocks), b(gc::RT_THREADS);
-    switch (vpl) {
-    case 1: hipLaunchKernelGGL((gc::route_kernel<1, BF16, ONE>), g, b, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((gc::route_kernel<2, BF16, ONE>), g, b, 0, st, a); break;
-    case 4: hipLaunchKernelGGL((gc::route_kernel<4, BF16, ONE>), g, b, 0, st, a); break;
-    case 8: hipLaunchKernelGGL((gc::route_kernel<8, BF16, ONE>), g, b, 0, st, a); break;
-    default: hipLaunchKernelGGL((gc::route_kernel<16, BF16, ONE>), g, b, 0, st, a); break;
+    if (route_lanes(a.E) == 64) {
+        if (route_values(a.E) == 8)
+            hipLaunchKernelGGL((gc::route_kernel<64, 8, BF16, ONE>), g, b, 0, st, a);
+        else
+            hipLaunchKernelGGL((gc::route_kernel<64, 16, BF16, ONE>), g, b, 0, st, a);
+        return;
+    }
+    switch (route_values(a.E)) {
+    case 1: hipLaunchKernelGGL((gc::route_kernel<16, 1, BF16, ONE>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gc::route_kernel<16, 2, BF16, ONE>), g, b, 0, st, a); break;
+    case 4: hipLaunchKernelGGL((gc::route_kernel<16, 4, BF16, ONE>), g, b, 0, st, a); break;
+    case 8: hipLaunchKernelGGL((gc::route_kernel<16, 8, BF16, ONE>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((gc::route_kernel<16, 16, BF16, ONE>), g, b, 0, st, a); break;
     }
 }
 
-// Routing (vpl > 0) and grouping of a.T * a.k items.
-int route_and_group(gc::RouteArgs &a, int vpl, bool bf16, void *workspace, uint64_t bytes,
+// Routing (with logits) and grouping of a.T * a.k items.
+int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, uint64_t bytes,
                     hipStream_t st)
 {
     const int64_t items = (int64_t)a.T * a.k;
     if (items <= gc::ROUTE_ONE_ITEMS) {
-        if (vpl == 0)
-            hipLaunchKernelGGL((gc::route_kernel<0, false, true>), dim3(1), dim3(gc::RT_THREADS), 0, st, a);
+        if (!route)
+            hipLaunchKernelGGL((gc::route_kernel<16, 0, false, true>), dim3(1), dim3(gc::RT_THREADS), 0, st, a);
         else if (bf16)
-            launch_route<true, true>(a, vpl, 1, st);
+            launch_route<true, true>(a, 1, st);
         else
-            launch_route<false, true>(a, vpl, 1, st);
+            launch_route<false, true>(a, 1, st);
         return launched();
     }
     // Blocks of consecutive tokens: about 512 items each, at most RT_BLOCKS.
@@ -97,12 +115,12 @@ int route_and_group(gc::RouteArgs &a, int vpl, bool bf16, void *workspace, uint6
             return GC_EINVAL;
         a.counts = (uint16_t *)((char *)workspace + kCountBytes);
     }
-    if (vpl == 0)
-        hipLaunchKernelGGL((gc::route_kernel<0, false, false>), dim3(blocks), dim3(gc::RT_THREADS), 0, st, a);
+    if (!route)
+        hipLaunchKernelGGL((gc::route_kernel<16, 0, false, false>), dim3(blocks), dim3(gc::RT_THREADS), 0, st, a);
     else if (bf16)
-        launch_route<true, false>(a, vpl, blocks, st);
+        launch_route<true, false>(a, blocks, st);
     else
-        launch_route<false, false>(a, vpl, blocks, st);
+        launch_route<false, false>(a, blocks, st);
     if (a.offsets)
         hipLaunchKernelGGL(gc::place_kernel, dim3(blocks), dim3(gc::RT_THREADS), 0, st, a);
     return launched();
@@ -152,9 +170,9 @@ void launch_sums(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hipStream_
     if (rows_per_group <= 16)
         launch_sums_rows<NB, 1, 4>(a, cus, st);
     else if (rows_per_group <= 32)
-        launch_sums_rows<NB, 2, 3>(a, cus, st);
+        launch_sums_rows<NB, 2, NB == 8 ? 3 : 4>(a, cus, st);
     else
-        launch_sums_rows<NB, 4, 3>(a, cus, st);
+        launch_sums_rows<NB, 4, NB == 8 ? 3 : 4>(a, cus, st);
 }
 
 template <bool GLU>
@@ -164,15 +182,43 @@ void launch_tiles(gc::GroupedArgs &a, int cus, hipStream_t st)
     hipLaunchKernelGGL((gc::tile_kernel<GLU>), dim3(cus), dim3(gc::NT), 0, st, a);
 }
 
-template <int RB>
-void launch_expand(const gc::ExpandArgs &a, int grid, hipStream_t st)
+void launch_expand(gc::ExpandArgs &a, int cus, hipStream_t st)
 {
-    const dim3 g(grid), b(gc::EX_THREADS);
-    switch ((a.r + 31) / 32) {
-    case 1: hipLaunchKernelGGL((gc::expand_kernel<RB, 1>), g, b, 0, st, a); break;
-    case 2: hipLaunchKernelGGL((gc::expand_kernel<RB, 2>), g, b, 0, st, a); break;
-    case 3: hipLaunchKernelGGL((gc::expand_kernel<RB, 3>), g, b, 0, st, a); break;
-    default: hipLaunchKernelGGL((gc::expand_kernel<RB, 4>), g, b, 0, st, a); break;
+    const dim3 b(gc::EX_THREADS);
+    const int steps = (a.r + 31) / 32;
+    if ((a.M + a.E - 1) / a.E >= 32) {
+        // Rows per workgroup: the fewest (of 16 to 128) with which all
+        // workgroups have a place at once, two per CU (one for r > 64).
+        a.spans = (a.N + gc::XR_COLS - 1) / gc::XR_COLS;
+        const int64_t places = (int64_t)cus * (steps <= 2 ? 2 : 1);
+        auto units = [&](int rows) {
+            return std::min<int64_t>(a.M, (a.M + rows - 1) / rows + a.E) * a.spans;
+        };
+        a.span = 16;
+        while (a.span < gc::XR_ROWS && units(a.span) > places)
+            a.span += 16;
+        const dim3 g((unsigned)std::min<int64_t>(units(a.span), places));
+        switch (steps) {
+        case 1: hipLaunchKernelGGL((gc::expand_rows_kernel<1>), g, b, 0, st, a); break;
+        case 2: hipLaunchKernelGGL((gc::expand_rows_kernel<2>), g, b, 0, st, a); break;
+        case 3: hipLaunchKernelGGL((gc::expand_rows_kernel<3>), g, b, 0, st, a); break;
+        default: hipLaunchKernelGGL((gc::expand_rows_kernel<4>), g, b, 0, st, a); break;
+        }
+        return;
+    }
+    // Spans of columns: at most as many workgroups as have a place at once.
+    const int64_t places = (int64_t)cus * gc::expand_resident(steps);
+    const int64_t tiles_n = (a.N + gc::EX_COLS - 1) / gc::EX_COLS;
+    const int64_t tiles_m = std::min<int64_t>(a.M, (a.M + 15) / 16 + a.E);
+    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, places / tiles_m));
+    a.span = (int)((tiles_n + want - 1) / want);
+    a.spans = (int)((tiles_n + a.span - 1) / a.span);
+    const dim3 g((unsigned)std::min<int64_t>(tiles_m * a.spans, (int64_t)cus * 8));
+    switch (steps) {
+    case 1: hipLaunchKernelGGL((gc::expand_kernel<1>), g, b, 0, st, a); break;
+    case 2: hipLaunchKernelGGL((gc::expand_kernel<2>), g, b, 0, st, a); break;
+    case 3: hipLaunchKernelGGL((gc::expand_kernel<3>), g, b, 0, st, a); break;
+    default: hipLaunchKernelGGL((gc::expand_kernel<4>), g, b, 0, st, a); break;
     }
 }
 
@@ -218,9 +264,7 @@ int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int
         return GC_EINVAL;
     if (T == 0 && !group)
         return GC_OK;
-    int vpl = 1;
-    while (vpl * 64 < E)
-        vpl *= 2;
+    const int v = route_values(E);
     gc::RouteArgs a = {};
     a.logits = logits;
     a.stride = stride;
@@ -236,8 +280,8 @@ int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int
     a.offsets = offsets;
     a.rows = rows;
     a.slots = slots;
-    a.vec = E % vpl == 0 && stride % vpl == 0 && aligned(logits, std::min<uintptr_t>(16, vpl * elem));
-    return route_and_group(a, vpl, logits_type == GC_BF16, workspace, workspace_bytes, (hipStream_t)stream);
+    a.vec = E % v == 0 && stride % v == 0 && aligned(logits, std::min<uintptr_t>(16, v * elem));
+    return route_and_group(a, true, logits_type == GC_BF16, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32_t *offsets,
@@ -258,7 +302,7 @@ int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32
     a.offsets = offsets;
     a.rows = rows;
     a.slots = slots;
-    return route_and_group(a, 0, false, workspace, workspace_bytes, (hipStream_t)stream);
+    return route_and_group(a, false, false, workspace, workspace_bytes, (hipStream_t)stream);
 }
 
 int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const int32_t *offsets,
@@ -409,19 +453,7 @@ int gemm_coll_lora_add(const gc_bf16 *base, const gc_bf16 *X, const gc_bf16 *dow
     x.r = r;
     x.E = G;
     x.copy = out != base;
-    // Spans: as many workgroups as the CUs hold at once (three each), for every
-    // span adds up its rows' H again.
-    const int bm = avg >= 24 ? 32 : 16;
-    const int64_t tiles_n = (N + gc::EX_COLS - 1) / gc::EX_COLS;
-    const int64_t tiles_m = std::min<int64_t>(M, (M + bm - 1) / bm + G);
-    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, 3 * cus / tiles_m));
-    x.span = (int)((tiles_n + want - 1) / want);
-    x.spans = (int)((tiles_n + x.span - 1) / x.span);
-    const int grid = (int)std::min<int64_t>(tiles_m * x.spans, (int64_t)cus * 8);
-    if (bm == 32)
-        launch_expand<2>(x, grid, st);
-    else
-        launch_expand<1>(x, grid, st);
+    launch_expand(x, cus, st);
     return launched();
 }
 

@@ -7,12 +7,19 @@
 // rounding would be as large as that of the output.
 //
 // Rows are read and written once and there are at most r <= 128 products per
-// output: the kernel is bound by the traffic of base and out.  A wave takes
-// 16*RB positions, whose H it adds up and keeps in registers, and walks over
-// blocks of 64 columns by itself, without a barrier: while it multiplies and
-// stores one block, the next block's rows of base (into registers) and r x 64
-// values of up (into LDS, in the layout the transposing read wants) are on
-// their way.
+// output: the kernels are bound by the traffic of base and out.  In both, the
+// products pass through LDS from the matrix cores' layout (a lane: 4 columns
+// of a row) to whole lines, so that a wave's load of base and its store of
+// out cover rows of 128 bytes and more.
+//
+// expand_rows_kernel, many rows per group: a wave keeps r x 128 values of up
+// in registers and walks down the rows of its workgroup, whose H stands in LDS
+// as bf16; nothing but rows of base and out moves in the loop, and the next
+// rows are on their way while these are multiplied.  (With up in LDS and the
+// walk along the columns, every tile of 256 columns waited for its block of
+// up, its base and the last stores in turn: M = 4096, N = 6288, r = 64 took
+// 44 us.)
+// expand_kernel, few rows per group: 16 positions, walking along the columns.
 #pragma once
 
 #include "grouped.hpp"
@@ -31,15 +38,65 @@ struct ExpandArgs {
     const int32_t *rows;       // [M]
     int M, N, r, E, splits;
     int copy;                  // out is not base: rows without adapter are copied
-    int span, spans;           // column tiles of EX_COLS a workgroup walks; spans per row tile
+    int span, spans;           // expand_kernel: column tiles of EX_COLS a workgroup walks, spans
+                               // per row tile; expand_rows_kernel: rows a workgroup walks,
+                               // column tiles of XR_COLS
 };
 
-// KS: steps of 32 that cover r.
-template <int RB, int KS>
-__global__ __launch_bounds__(EX_THREADS) void expand_kernel(ExpandArgs p)
+// Eight neighbouring outputs: fp32 products a, b plus base, rounded once.
+__device__ __forceinline__ u32x4_t add_base(f32x4_t a, f32x4_t b, u32x4_t base)
 {
-    constexpr int BM = 16 * RB, NB = 4, BN = 64;
-    __shared__ __attribute__((aligned(1024))) uint8_t ups[EX_WAVES * KS * 4096];
+    const u32x2_t x = pack_bf16x4(a + unpack_bf16x4((u32x2_t){base[0], base[1]}));
+    const u32x2_t y = pack_bf16x4(b + unpack_bf16x4((u32x2_t){base[2], base[3]}));
+    return (u32x4_t){x[0], x[1], y[0], y[1]};
+}
+
+// Eight neighbouring values of H for position m: the sums over the pieces of
+// K, in order, times the scale, as two bf16 whose sum carries 16 bits.
+template <int AHEAD>
+__device__ __forceinline__ void load_h(const ExpandArgs &p, bool on, int m, int k, float scale, u32x4_t &hi,
+                                       u32x4_t &lo)
+{
+    f32x4_t x = {0.f, 0.f, 0.f, 0.f}, y = x;
+    const float *at = p.sums + (on ? (size_t)m * p.r + k : 0);
+    for (int c = 0; c < p.splits; c += AHEAD) {
+        f32x4_t a[AHEAD], b[AHEAD];
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            a[d] = b[d] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+            if (on && c + d < p.splits) {
+                const float *q = at + (size_t)(c + d) * p.M * p.r;
+                a[d] = *(const f32x4_t *)q;
+                b[d] = *(const f32x4_t *)(q + 4);
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < AHEAD; ++d) {
+            x += a[d];
+            y += b[d];
+        }
+    }
+    x *= scale;
+    y *= scale;
+    const u32x2_t hx = pack_bf16x4(x), hy = pack_bf16x4(y);
+    const u32x2_t lx = pack_bf16x4(x - unpack_bf16x4(hx)), ly = pack_bf16x4(y - unpack_bf16x4(hy));
+    hi = (u32x4_t){hx[0], hx[1], hy[0], hy[1]};
+    lo = (u32x4_t){lx[0], lx[1], ly[0], ly[1]};
+}
+
+// Workgroups that a CU holds at once (their blocks of up fill its LDS).
+constexpr int expand_resident(int steps) { return steps <= 2 ? 3 : steps == 3 ? 2 : 1; }
+
+// KS: steps of 32 that cover r.
+template <int KS>
+__global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel(ExpandArgs p)
+{
+    constexpr int BM = 16;
+    constexpr int UP = KS * 32 * EX_COLS * 2;            // bytes of a block of up
+    constexpr int LOADS = KS * 16 / EX_WAVES;            // of up, per wave
+    constexpr int PITCH = 64 * 4 + 16;                   // bytes of a row in the exchange
+    __shared__ __attribute__((aligned(1024))) uint8_t ups[UP];
+    __shared__ __attribute__((aligned(16))) uint8_t exchange[EX_WAVES * 16 * PITCH];
     __shared__ int first[GR_GROUPS + 1];
     __shared__ int wsum[EX_THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -51,12 +108,12 @@ __global__ __launch_bounds__(EX_THREADS) void expand_kernel(ExpandArgs p)
     const uint32_t N2 = (uint32_t)p.N * 2u;
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base, (uint32_t)p.M * N2);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.M * N2);
-    const uint32_t mine = lds_addr(ups) + (uint32_t)(wave * KS * 4096);
-    // layout of a 32 x 64 block as in stream_kernel for NB = 4
-    auto fold = [](int k) { return ((k >> 1) & 1) | (((k >> 3) & 1) << 1); };
-    const int b_row = lane >> 3, b_slot = lane & 7;
-    const int f_lane = fold(8 * fg + (fi >> 2));
-    const int p8 = 8 * (fg >> 1) + 16 * (fg & 1);
+    const uint32_t ups0 = lds_addr(ups);
+    uint8_t *const ex = exchange + wave * 16 * PITCH;
+    // block of up: 512-byte rows, the 32-byte chunk c of row k kept at chunk
+    // c ^ f(k) (see run_tile)
+    const int slot = lane & 31;
+    const int fB = (fi >> 2) | ((fg & 1) << 2);
 
     for (int t = blockIdx.x; t < units; t += gridDim.x) {
         const int e = __builtin_amdgcn_readfirstlane(find_group(first, groups, t, lane));
@@ -66,127 +123,235 @@ __global__ __launch_bounds__(EX_THREADS) void expand_kernel(ExpandArgs p)
         hi = __builtin_amdgcn_readfirstlane(hi);
         const int in = t - __builtin_amdgcn_readfirstlane(first[e]);
         const int mt = in / p.spans;
-        int n0 = (in - mt * p.spans) * p.span * EX_COLS + wave * BN;
-        const int n_end = min(p.N, n0 - wave * BN + p.span * EX_COLS);
+        const int n_begin = (in - mt * p.spans) * p.span * EX_COLS;
+        const int n_end = min(p.N, n_begin + p.span * EX_COLS);
         const int m0 = lo + mt * BM;
         const bool delta = e < p.E;
-        const u32x4_t ru = make_rsrc4(p.up + (size_t)(delta ? e : 0) * p.r * p.N, delta ? (uint32_t)p.r * N2 : 0u);
+        const u32x4_t ru =
+            make_rsrc4(p.up + (size_t)(delta ? e : 0) * p.r * p.N, delta ? (uint32_t)p.r * N2 : 0u);
         auto load_up = [&](int n0) {
 #pragma unroll
-            for (int i = 0; i < 4 * KS; ++i) {
-                const int k = 8 * i + b_row;
-                const int n = n0 + 16 * ((b_slot >> 1) ^ fold(k)) + 8 * (b_slot & 1);
-                dma16(ru, mine + i * 1024, n < n_end ? (uint32_t)k * N2 + (uint32_t)n * 2u : OOB);
+            for (int i = 0; i < LOADS; ++i) {
+                const int k = 2 * (wave * LOADS + i) + (lane >> 5);
+                const int fk = (k & 3) | (((k >> 3) & 1) << 2);
+                const int n = n0 + 16 * ((slot >> 1) ^ fk) + 8 * (slot & 1);
+                dma16(ru, ups0 + (uint32_t)((wave * LOADS + i) * 1024),
+                      n < n_end ? (uint32_t)k * N2 + (uint32_t)n * 2u : OOB);
             }
         };
-        uint32_t row_off[RB];
+        // base and out: instruction i covers rows 8 i + lane / 8 of the wave's
+        // 16, columns 8 (lane % 8) .. + 7 of a group of 64
+        uint32_t row_off[2];
 #pragma unroll
-        for (int i = 0; i < RB; ++i) {
-            const int m = m0 + 16 * i + fi;
+        for (int i = 0; i < 2; ++i) {
+            const int m = m0 + 8 * i + (lane >> 3);
             int row = -1;
             if (m >= lo && m < hi)
                 row = p.rows[m];
-            row_off[i] = (unsigned)row < (unsigned)p.M ? (uint32_t)row * N2 + (uint32_t)p8 * 2u : OOB;
+            row_off[i] =
+                (unsigned)row < (unsigned)p.M ? (uint32_t)row * N2 + (uint32_t)(lane & 7) * 16u : OOB;
         }
-        auto offset = [&](int i, int h, int n0) {
-            return n0 + p8 + 32 * h < n_end ? row_off[i] + (uint32_t)(n0 + 32 * h) * 2u : OOB;
+        auto offset = [&](int i, int n0) {
+            const int n = n0 + 64 * wave;
+            return n + 8 * (lane & 7) < n_end ? row_off[i] + (uint32_t)n * 2u : OOB;
         };
-        auto load_base = [&](u32x4_t (&old)[RB][2], int n0) {
+        load_up(n_begin);
+        u32x4_t old[2];
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    old[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(i, h, n0), 0, 0);
-        };
-        wait_lgkmcnt0();                         // the last unit's block of up is read
-        load_up(n0);
-        u32x4_t old[RB][2];
-        load_base(old, n0);
+        for (int i = 0; i < 2; ++i)
+            old[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(i, n_begin), 0, 0);
         // H of the rows, as two bf16 fragments
-        bf16x8_t h[RB][KS], l[RB][KS];
-        {
-            const float sc = delta ? p.scale[e] : 0.f;
+        bf16x8_t h[KS], l[KS];
+        const float sc = delta ? p.scale[e] : 0.f;
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int m = m0 + 16 * i + fi, k = 32 * s + 8 * fg;
-                    f32x4_t x = {0.f, 0.f, 0.f, 0.f}, y = x;
-                    if (delta && m < hi && k < p.r) {
-                        const float *at = p.sums + (size_t)m * p.r + k;
-                        for (int c = 0; c < p.splits; ++c, at += (size_t)p.M * p.r) {
-                            x += *(const f32x4_t *)at;
-                            y += *(const f32x4_t *)(at + 4);
-                        }
-                    }
-                    x *= sc;
-                    y *= sc;
-                    const u32x2_t hx = pack_bf16x4(x), hy = pack_bf16x4(y);
-                    const u32x2_t lx = pack_bf16x4(x - unpack_bf16x4(hx)), ly = pack_bf16x4(y - unpack_bf16x4(hy));
-                    h[i][s] = __builtin_bit_cast(bf16x8_t, (u32x4_t){hx[0], hx[1], hy[0], hy[1]});
-                    l[i][s] = __builtin_bit_cast(bf16x8_t, (u32x4_t){lx[0], lx[1], ly[0], ly[1]});
-                }
+        for (int s = 0; s < KS; ++s) {
+            const int m = m0 + fi, k = 32 * s + 8 * fg;
+            u32x4_t a, b;
+            load_h<KS == 1 ? 8 : 4>(p, delta && m < hi && k < p.r, m, k, sc, a, b);
+            h[s] = __builtin_bit_cast(bf16x8_t, a);
+            l[s] = __builtin_bit_cast(bf16x8_t, b);
         }
-        for (; n0 < n_end; n0 += EX_COLS) {
-            wait_vmcnt<0>();                     // this block of up has landed
-            bf16x8_t fa[KS][NB];
+        for (int n0 = n_begin; n0 < n_end; n0 += EX_COLS) {
+            wait_vmcnt<0>();                     // this wave's part of the block of up has landed,
+            __syncthreads();                     // now everybody's
+            f32x4_t acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const uint32_t a = mine + (uint32_t)(s * 4096 + (8 * fg + (fi >> 2)) * 128 + 8 * (fi & 3) +
-                                                         ((j ^ f_lane) * 32));
+                for (int j = 0; j < 4; ++j) {
+                    const int q = 4 * wave + j;                        // 32-byte chunk
+                    const uint32_t a = ups0 + (uint32_t)((32 * s + 8 * fg + (fi >> 2)) * 512 + 8 * (fi & 3) +
+                                                         (q >> 3) * 256 + (((q & 7) ^ fB) * 32));
                     bf16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
                         (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a));
                     bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
-                        (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a + 4 * 128));
-                    fa[s][j] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                        (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a + 4 * 512));
+                    const bf16x8_t fa = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s], acc[j], 0, 0, 0);
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, l[s], acc[j], 0, 0, 0);
                 }
-            wait_lgkmcnt0();
-            u32x4_t next[RB][2];
-            load_up(n0 + EX_COLS);               // (past the end: empty)
-            load_base(next, n0 + EX_COLS);
-            f32x4_t acc[RB][NB];
+            // (LDS operations of a wave are done in order: no wait between them)
 #pragma unroll
-            for (int i = 0; i < RB; ++i)
+            for (int j = 0; j < 4; ++j)
+                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = acc[j];
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
-                    acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int s = 0; s < KS; ++s)
-#pragma unroll
-                for (int i = 0; i < RB; ++i)
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h[i][s], acc[i][j], 0, 0, 0);
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], l[i][s], acc[i][j], 0, 0, 0);
-                    }
-            // fp32 sums regrouped as in pack_pair (lanes trade halves so that
-            // each holds 8 consecutive columns), base added, one rounding
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    f32x4_t a, b;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const auto sw = __builtin_amdgcn_permlane16_swap(
-                            __float_as_uint(acc[i][2 * g][c]), __float_as_uint(acc[i][2 * g + 1][c]), false, false);
-                        a[c] = __uint_as_float(sw[0]);
-                        b[c] = __uint_as_float(sw[1]);
-                    }
-                    const u32x4_t o = old[i][g];
-                    const u32x2_t x = pack_bf16x4(a + unpack_bf16x4((u32x2_t){o[0], o[1]}));
-                    const u32x2_t y = pack_bf16x4(b + unpack_bf16x4((u32x2_t){o[2], o[3]}));
-                    store16(ro, offset(i, g, n0), (u32x4_t){x[0], x[1], y[0], y[1]});
-                }
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-#pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    old[i][g] = next[i][g];
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t *at = ex + (8 * i + (lane >> 3)) * PITCH + (lane & 7) * 32;
+                store16(ro, offset(i, n0), add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]));
+                // (past the end: an empty load)
+                old[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(i, n0 + EX_COLS), 0, 0);
+            }
+            __builtin_amdgcn_wave_barrier();
+            __syncthreads();                     // the block of up is read
+            if (n0 + EX_COLS < n_end)
+                load_up(n0 + EX_COLS);
         }
-        wait_vmcnt<0>();                         // the empty loads have written their zeros
+    }
+}
+
+constexpr int XR_COLS = 512, XR_ROWS = 128;              // columns, and most rows, of a workgroup
+
+template <int KS>
+__global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kernel(ExpandArgs p)
+{
+    constexpr int NB = 8;                                // 16-column blocks of a wave
+    constexpr int H_PITCH = 64 * KS + 16;                // bytes of a row of H in LDS
+    constexpr int PITCH = 128 * 4 + 16;                  // bytes of a row in the exchange
+    constexpr int MINE = 16 * PITCH;                     // bytes of a wave: a block of up, later the exchange
+    static_assert(MINE >= 32 * 256, "a block of up");
+    __shared__ __attribute__((aligned(1024))) uint8_t own[EX_WAVES * MINE];
+    __shared__ __attribute__((aligned(16))) uint8_t h_hi[XR_ROWS * H_PITCH], h_lo[XR_ROWS * H_PITCH];
+    __shared__ uint32_t s_row[XR_ROWS + 16];             // byte offset of each row in base and out
+    __shared__ int first[GR_GROUPS + 1];
+    __shared__ int wsum[EX_THREADS / 64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int fi = lane & 15, fg = lane >> 4;
+    const int groups = p.E + (p.copy ? 1 : 0);
+    const int units =
+        scan_tiles<EX_THREADS>(p.offsets, p.E, p.M, groups, p.span, p.spans, first, wsum);
+    const uint32_t N2 = (uint32_t)p.N * 2u;
+    const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base, (uint32_t)p.M * N2);
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.M * N2);
+    const uint32_t mine = lds_addr(own) + (uint32_t)(wave * MINE);
+    uint8_t *const ex = own + wave * MINE;
+    // block of up: 32 rows of 256 bytes, as stream_kernel's for NB = 8
+    auto fold = [](int k) { return (k & 3) | (((k >> 3) & 1) << 2); };
+    const int b_row = lane >> 4, b_slot = lane & 15;
+    const int f_lane = fold(8 * fg + (fi >> 2));
+
+    for (int t = blockIdx.x; t < units; t += gridDim.x) {
+        const int e = __builtin_amdgcn_readfirstlane(find_group(first, groups, t, lane));
+        int lo, hi;
+        group_range(p.offsets, p.E, p.M, e, lo, hi);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        hi = __builtin_amdgcn_readfirstlane(hi);
+        const int in = t - __builtin_amdgcn_readfirstlane(first[e]);
+        const int mt = in / p.spans;
+        const int n0 = (in - mt * p.spans) * XR_COLS + 128 * wave;
+        const int m0 = lo + mt * p.span;
+        const int count = min(hi - m0, p.span);          // rows of this workgroup
+        const bool delta = e < p.E;
+        const u32x4_t ru =
+            make_rsrc4(p.up + (size_t)(delta ? e : 0) * p.r * p.N, delta ? (uint32_t)p.r * N2 : 0u);
+        auto load_up = [&](int s) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                const int k = 4 * i + b_row;
+                const int n = n0 + 16 * ((b_slot >> 1) ^ fold(k)) + 8 * (b_slot & 1);
+                dma16(ru, mine + i * 1024, n < p.N ? (uint32_t)(32 * s + k) * N2 + (uint32_t)n * 2u : OOB);
+            }
+        };
+        load_up(0);
+        for (int i = tid; i < XR_ROWS + 16; i += EX_THREADS) {
+            int row = -1;
+            if (i < count)
+                row = p.rows[m0 + i];
+            s_row[i] = (unsigned)row < (unsigned)p.M ? (uint32_t)row * N2 : OOB;
+        }
+        // H of the workgroup's rows, 8 values a time
+        if (delta) {
+            const float sc = p.scale[e];
+            for (int i = tid; i < (count + 15) / 16 * 16 * 4 * KS; i += EX_THREADS) {
+                const int r = i / (4 * KS), k = 8 * (i - r * 4 * KS);
+                u32x4_t a, b;
+                load_h<4>(p, r < count && k < p.r, m0 + r, k, sc, a, b);
+                *(u32x4_t *)(h_hi + r * H_PITCH + 2 * k) = a;
+                *(u32x4_t *)(h_lo + r * H_PITCH + 2 * k) = b;
+            }
+        }
+        bf16x8_t fa[KS][NB];
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            wait_vmcnt<0>();
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                const uint32_t a =
+                    mine + (uint32_t)((8 * fg + (fi >> 2)) * 256 + 8 * (fi & 3) + ((j ^ f_lane) * 32));
+                bf16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                    (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a));
+                bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
+                    (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a + 4 * 256));
+                fa[s][j] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            }
+            wait_lgkmcnt0();                             // read before it is filled again
+            if (s + 1 < KS)
+                load_up(s + 1);
+        }
+        __syncthreads();                                 // rows and H are there
+        // instruction i of a block of 16 rows: rows 4 i + lane / 16, columns
+        // 8 (lane % 16) .. + 7 of the wave's 128
+        const int nc = n0 + 8 * (lane & 15);
+        auto offset = [&](int b, int i) {
+            const uint32_t o = s_row[16 * b + 4 * i + (lane >> 4)];
+            return nc < p.N && o != OOB ? o + (uint32_t)nc * 2u : OOB;
+        };
+        const int blocks = (count + 15) / 16;
+        u32x4_t old[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            old[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(0, i), 0, 0);
+        for (int b = 0; b < blocks; ++b) {
+            // the next block's rows (past the last: s_row holds none)
+            u32x4_t next[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                next[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(b + 1, i), 0, 0);
+            f32x4_t acc[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+            if (delta) {
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    const int at = (16 * b + fi) * H_PITCH + 2 * (32 * s + 8 * fg);
+                    const bf16x8_t h = *(const bf16x8_t *)(h_hi + at), l = *(const bf16x8_t *)(h_lo + at);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h, acc[j], 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], l, acc[j], 0, 0, 0);
+                }
+            }
+            // (LDS operations of a wave are done in order: no wait between them)
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = acc[j];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *at = ex + (4 * i + (lane >> 4)) * PITCH + (lane & 15) * 32;
+                store16(ro, offset(b, i), add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]));
+                old[i] = next[i];
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        __syncthreads();                                 // rows and H are read
     }
 }
 

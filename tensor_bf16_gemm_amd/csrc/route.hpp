@@ -7,11 +7,16 @@
 // sigmoid(logit) in fp32.  A logit of NaN or -inf is never chosen; a place
 // that is left over gets id -1 and weight 0.
 //
-// One wave per token: lane l holds the VPL consecutive experts VPL*l ..
-// VPL*l + VPL-1 as order-preserving 32-bit keys, so "lowest index first" is
-// "lowest lane first".  Each of the k rounds is one maximum over the wave
-// (six DPP steps), one ballot, and the removal of the winner; nothing is
-// sorted and nothing leaves the registers.
+// A token is a row of 16 lanes (four tokens per wave) for up to 256 experts,
+// else a whole wave; each lane holds V consecutive experts.  A (key, index)
+// pair is packed into the mantissa of a double in [1, 2) -- 32 bits of an
+// order-preserving key, then the index counted downwards -- so that one
+// v_max_f64 compares both and no two are equal.  Every lane sorts its V pairs
+// once (a network of min/max); a round of the choice is then a maximum over
+// the lanes' heads (four row rotations) and the winner's lane moves its list
+// up by one.  About 120 instructions per token at E = 256, k = 8, where the
+// rounds of a whole wave per token took 560 and the issue rate bound them
+// (16384 tokens: 16.8 us; this way LATER).
 //
 // Grouping: a stable counting sort by blocks of consecutive items.  Counts
 // per block first (LDS integer atomics: order does not matter to a sum), then
@@ -22,6 +27,8 @@
 // bit of the group number.  Up to ROUTE_ONE_ITEMS items take one workgroup and
 // one launch for everything.
 #pragma once
+
+#include <utility>
 
 #include "gc_kernel.hpp"
 
@@ -55,35 +62,73 @@ struct RouteArgs {
     bool vec;                // a lane's VPL logits are whole aligned vectors
 };
 
-// Lane 63 of the wave's running maximum / sum (DPP row shifts, then the two
-// row broadcasts), as a uniform value.
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v)
+// v of the lane ROR places down in the row of 16 (cyclic).
+template <int ROR>
+__device__ __forceinline__ uint32_t row_ror(uint32_t v)
 {
-    auto mx = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false));
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false));
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false));
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false));
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false));
-    v = mx(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROR, 0xf, 0xf, true);
 }
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_add(float v)
+// Maximum over the LPT lanes of a token (a row of 16, or the wave), in all of
+// them; the pairs are never NaN.
+template <int ROR>
+__device__ __forceinline__ double ror_max(double v)
 {
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint64_t o = ((uint64_t)row_ror<ROR>((uint32_t)(b >> 32)) << 32) | row_ror<ROR>((uint32_t)b);
+    return fmax(v, __longlong_as_double((long long)o));
+}
+// (the two halves of a swap with itself: the rows, or the wave halves, side by side)
+template <bool HALVES>
+__device__ __forceinline__ double swap_max(double v)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    const uint32_t lo = (uint32_t)b, hi = (uint32_t)(b >> 32);
+    uint64_t x, y;
+    if (HALVES) {
+        const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false);
+        const auto h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        x = ((uint64_t)h[0] << 32) | l[0];
+        y = ((uint64_t)h[1] << 32) | l[1];
+    } else {
+        const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false);
+        const auto h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        x = ((uint64_t)h[0] << 32) | l[0];
+        y = ((uint64_t)h[1] << 32) | l[1];
+    }
+    return fmax(__longlong_as_double((long long)x), __longlong_as_double((long long)y));
+}
+template <int LPT>
+__device__ __forceinline__ double token_max(double v)
+{
+    v = ror_max<8>(v);
+    v = ror_max<4>(v);
+    v = ror_max<2>(v);
+    v = ror_max<1>(v);
+    if (LPT == 64) {
+        v = swap_max<false>(v);
+        v = swap_max<true>(v);
+    }
+    return v;
 }
 
-__device__ __forceinline__ float wave_sum(float v)
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v)
 {
-    v = dpp_add<0x111, 0xf>(v);
-    v = dpp_add<0x112, 0xf>(v);
-    v = dpp_add<0x114, 0xf>(v);
-    v = dpp_add<0x118, 0xf>(v);
-    v = dpp_add<0x142, 0xa>(v);
-    v = dpp_add<0x143, 0xc>(v);
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    auto ror = [](float x, auto c) {
+        return __uint_as_float(row_ror<decltype(c)::value>(__float_as_uint(x)));
+    };
+    v += ror(v, std::integral_constant<int, 8>{});
+    v += ror(v, std::integral_constant<int, 4>{});
+    v += ror(v, std::integral_constant<int, 2>{});
+    v += ror(v, std::integral_constant<int, 1>{});
+    if (LPT == 64) {
+        const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+        const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+        v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    }
+    return v;
 }
 
 // Inclusive prefix sum over the lanes of a wave.
@@ -123,134 +168,170 @@ __device__ __forceinline__ float soft_term(float x, float high)
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// Tokens that a wave routes side by side: a round is a chain of some twenty
-// dependent steps (the maximum over the wave, the ballot, the removal), which
-// one token alone would wait through.
-template <int VPL>
-constexpr int ROUTE_TOK = VPL <= 4 ? 4 : VPL == 8 ? 2 : 1;
-
-// Routes tokens t, t + RT_WAVES, ... (those below t1) in one wave.  Lane j < k
-// returns with the j-th choice's expert (-1: none) in id[] and its weight in w[].
-template <int VPL, bool BF16, int TOK>
-__device__ __forceinline__ void route_tokens(const RouteArgs &p, int t, int t1, int lane, int (&id)[TOK],
-                                             float (&w)[TOK])
+// The pair of an expert as a double in [1, 2); NO_PAIR, the least, for an
+// expert that cannot be chosen.
+constexpr uint64_t PAIR_ONE = 0x3FF0000000000000ull;
+__device__ __forceinline__ double make_pair(uint32_t key, int e)
 {
-    const int e0 = lane * VPL;
+    const uint64_t b = key > KEY_NEG_INF ? PAIR_ONE | ((uint64_t)key << 20) | (uint32_t)(RT_GROUPS - 1 - e)
+                                         : PAIR_ONE;
+    return __longlong_as_double((long long)b);
+}
+__device__ __forceinline__ uint32_t pair_key(double v)
+{
+    return (uint32_t)((uint64_t)__double_as_longlong(v) >> 20);
+}
+__device__ __forceinline__ int pair_expert(double v)
+{
+    return RT_GROUPS - 1 - (int)((uint64_t)__double_as_longlong(v) & 0xFFFFFu);
+}
+
+// Odd-even merge network (Batcher) for V a power of two: its comparators, as
+// a table the compiler unrolls.
+template <int V>
+struct MergeNetwork {
+    struct Pair {
+        int lo, hi;
+    };
+    static constexpr int count()
+    {
+        int n = 0;
+        for (int p = 1; p < V; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < V; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < V; ++i)
+                        n += (i + j) / (2 * p) == (i + j + k) / (2 * p);
+        return n;
+    }
+    static constexpr Pair pair(int which)
+    {
+        int n = 0;
+        for (int p = 1; p < V; p *= 2)
+            for (int k = p; k >= 1; k /= 2)
+                for (int j = k % p; j + k < V; j += 2 * k)
+                    for (int i = 0; i < k && i + j + k < V; ++i)
+                        if ((i + j) / (2 * p) == (i + j + k) / (2 * p) && n++ == which)
+                            return Pair{i + j, i + j + k};
+        return Pair{0, 0};
+    }
+};
+
+template <int V, int... I>
+__device__ __forceinline__ void sort_steps(double (&a)[V], std::integer_sequence<int, I...>)
+{
+    auto step = [&](auto c) {
+        constexpr auto at = MergeNetwork<V>::pair(decltype(c)::value);
+        const double hi = fmax(a[at.lo], a[at.hi]), lo = fmin(a[at.lo], a[at.hi]);
+        a[at.lo] = hi;
+        a[at.hi] = lo;
+    };
+    (step(std::integral_constant<int, I>{}), ...);
+}
+
+// Falling order.
+template <int V>
+__device__ __forceinline__ void sort_pairs(double (&a)[V])
+{
+    if constexpr (V > 1)
+        sort_steps(a, std::make_integer_sequence<int, MergeNetwork<V>::count()>{});
+}
+
+// mask ? x : y by bits.  (A conditional between neighbours of an array in
+// registers is turned into an index and a chain of compares.)
+__device__ __forceinline__ double pick(uint64_t mask, double x, double y)
+{
+    const uint64_t a = (uint64_t)__double_as_longlong(x), b = (uint64_t)__double_as_longlong(y);
+    return __longlong_as_double((long long)((a & mask) | (b & ~mask)));
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const RouteArgs &p, int t, int e)
+{
+    if (BF16)
+        return __uint_as_float((uint32_t)((const uint16_t *)p.logits)[(int64_t)t * p.stride + e] << 16);
+    return ((const float *)p.logits)[(int64_t)t * p.stride + e];
+}
+
+// Routes one token per LPT lanes.  Lane j < k of the token returns with the
+// j-th choice's expert (-1: none) in `id` and its weight in `w`.  `t` is the
+// lane's token, which must exist.
+template <int LPT, int V, bool BF16>
+__device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, int &id, float &w)
+{
+    const int e0 = j * V;
     const bool soft = p.score == SCORE_SOFTMAX;
-    float x[TOK][VPL], high[TOK], val[TOK];
-    uint32_t key[TOK][VPL];
-#pragma unroll
-    for (int q = 0; q < TOK; ++q) {
-        const int tq = t + q * RT_WAVES;
-        const bool live = tq < t1;
+    float x[V];
+    if (p.vec && e0 < p.E) {
         if constexpr (BF16) {
-            const uint16_t *row = (const uint16_t *)p.logits + (int64_t)(live ? tq : t) * p.stride;
-            uint16_t b[VPL];
-            if (p.vec && e0 < p.E) {
-                __builtin_memcpy(b, __builtin_assume_aligned(row + e0, VPL * 2 < 16 ? VPL * 2 : 16), sizeof b);
-            } else {
+            uint16_t b[V];
+            __builtin_memcpy(b, __builtin_assume_aligned((const uint16_t *)p.logits + (int64_t)t * p.stride + e0,
+                                                         V * 2 < 16 ? V * 2 : 16), sizeof b);
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    b[i] = e0 + i < p.E ? row[e0 + i] : (uint16_t)0xFF80;
-            }
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                x[q][i] = __uint_as_float((uint32_t)b[i] << 16);
+            for (int i = 0; i < V; ++i)
+                x[i] = __uint_as_float((uint32_t)b[i] << 16);
         } else {
-            const float *row = (const float *)p.logits + (int64_t)(live ? tq : t) * p.stride;
-            if (p.vec && e0 < p.E) {
-                __builtin_memcpy(x[q], __builtin_assume_aligned(row + e0, VPL * 4 < 16 ? VPL * 4 : 16),
-                                 sizeof x[q]);
-            } else {
+            __builtin_memcpy(x, __builtin_assume_aligned((const float *)p.logits + (int64_t)t * p.stride + e0,
+                                                         V * 4 < 16 ? V * 4 : 16), sizeof x);
+        }
+    } else {
 #pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    x[q][i] = e0 + i < p.E ? row[e0 + i] : -__builtin_huge_valf();
+        for (int i = 0; i < V; ++i)
+            x[i] = e0 + i < p.E ? logit<BF16>(p, t, e0 + i) : -__builtin_huge_valf();
+    }
+    double a[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        a[i] = make_pair(order_key(x[i]), e0 + i);
+    // For a softmax over all experts: its maximum and its sum.
+    float high = 0.f, total = 1.f;
+    if (soft && (p.bias || !p.renorm)) {
+        double m = a[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i)
+            m = fmax(m, a[i]);
+        high = key_value(pair_key(token_max<LPT>(m)));
+        float part = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            part += pair_key(a[i]) != 0 ? soft_term(x[i], high) : 0.f;
+        total = token_sum<LPT>(part);
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (pair_key(a[i]) != 0) {
+                const float s = soft ? soft_term(x[i], high) / total : sigmoid(x[i]);
+                a[i] = make_pair(order_key(s + p.bias[e0 + i]), e0 + i);
             }
-        }
     }
+    sort_pairs(a);
+    const double none = __longlong_as_double((long long)PAIR_ONE);
+    double mine = none, best = none;
+    for (int r = 0; r < p.k; ++r) {
+        const double top = token_max<LPT>(a[0]);
+        if (r == 0)
+            best = top;
+        mine = j == r ? top : mine;
+        const bool won = a[0] == top;            // (none: its list is empty, moving it changes nothing)
+        const uint64_t mask = won ? ~0ull : 0ull;
 #pragma unroll
-    for (int q = 0; q < TOK; ++q) {
-        high[q] = val[q] = 0.f;
-        id[q] = -1;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            key[q][i] = e0 + i < p.E ? order_key(x[q][i]) : 0u;
-        if (p.bias) {
-            // scores first, for their sum with the bias is what is compared
-            float total = 1.f;
-            if (soft) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    m = max(m, key[q][i]);
-                high[q] = key_value(wave_max_u32(m));
-                float part = 0.f;
-#pragma unroll
-                for (int i = 0; i < VPL; ++i)
-                    part += key[q][i] > KEY_NEG_INF ? soft_term(x[q][i], high[q]) : 0.f;
-                total = wave_sum(part);
-            }
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const bool any = key[q][i] > KEY_NEG_INF;
-                x[q][i] = !any ? 0.f : soft ? soft_term(x[q][i], high[q]) / total : sigmoid(x[q][i]);
-                key[q][i] = any ? order_key(x[q][i] + p.bias[e0 + i]) : 0u;
-            }
-        }
+        for (int i = 0; i + 1 < V; ++i)
+            a[i] = pick(mask, a[i + 1], a[i]);
+        a[V - 1] = pick(mask, none, a[V - 1]);
     }
-    for (int j = 0; j < p.k; ++j) {
-        uint32_t m[TOK], top[TOK];
-        int at[TOK];
-        float s[TOK];
-#pragma unroll
-        for (int q = 0; q < TOK; ++q) {
-            m[q] = key[q][0];
-            at[q] = 0;
-            s[q] = x[q][0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i)
-                if (key[q][i] > m[q]) {
-                    m[q] = key[q][i];
-                    at[q] = i;
-                    s[q] = x[q][i];
-                }
-        }
-#pragma unroll
-        for (int q = 0; q < TOK; ++q)
-            top[q] = wave_max_u32(m[q]);
-#pragma unroll
-        for (int q = 0; q < TOK; ++q) {
-            // (with nothing left, the lane found is given no choice below)
-            const int wl = __builtin_ctzll(__builtin_amdgcn_ballot_w64(m[q] == top[q]));
-            const int won = wl * VPL + __builtin_amdgcn_readlane(at[q], wl);
-            const float ws = p.bias ? __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s[q]), wl))
-                                    : key_value(top[q]);
-            const bool any = top[q] > KEY_NEG_INF;
-            if (j == 0 && !p.bias)
-                high[q] = ws;
-            id[q] = any && lane == j ? won : id[q];
-            val[q] = any && lane == j ? ws : val[q];
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                key[q][i] = lane == wl && i == at[q] ? 0u : key[q][i];
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < TOK; ++q) {
-        w[q] = id[q] < 0 ? 0.f : p.bias ? val[q] : soft ? soft_term(val[q], high[q]) : sigmoid(val[q]);
-        if (p.renorm) {
-            const float total = wave_sum(w[q]);
-            w[q] = total > 0.f ? w[q] / total : 0.f;
-        } else if (soft && !p.bias) {
-            float part = 0.f;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                part += e0 + i < p.E && order_key(x[q][i]) > KEY_NEG_INF ? soft_term(x[q][i], high[q]) : 0.f;
-            const float total = wave_sum(part);
-            w[q] = total > 0.f ? w[q] / total : 0.f;
-        }
-        w[q] *= p.scale;
-    }
+    const bool chosen = pair_key(mine) != 0;
+    id = chosen ? pair_expert(mine) : -1;
+    float val = key_value(pair_key(mine));
+    if (p.bias)
+        val = logit<BF16>(p, t, chosen ? id : 0);
+    else if (soft && p.renorm)
+        high = key_value(pair_key(best));
+    w = !chosen ? 0.f : soft ? soft_term(val, high) : sigmoid(val);
+    if (p.renorm)
+        total = token_sum<LPT>(w);
+    else if (!soft)
+        total = 1.f;
+    w = chosen && total > 0.f ? w / total * p.scale : 0.f;
 }
 
 // LDS of the grouping.
@@ -328,16 +409,16 @@ __device__ __forceinline__ int group_of(int id, int groups)
     return (unsigned)id < (unsigned)groups ? id : groups;
 }
 
-// Routes the tokens of this block (VPL > 0) or reads their ids (VPL == 0),
+// Routes the tokens of this block (V > 0) or reads their ids (V == 0),
 // then: ONE (a single workgroup, at most ROUTE_ONE_ITEMS items) groups them,
 // else counts them per group.
-template <int VPL, bool BF16, bool ONE>
+template <int LPT, int V, bool BF16, bool ONE>
 __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
 {
     static_assert(ROUTE_ONE_ITEMS <= RT_THREADS, "one item per thread");
     __shared__ GroupLds l;
     __shared__ int s_id[ONE ? ROUTE_ONE_ITEMS : 1];
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int t0 = ONE ? 0 : blockIdx.x * p.block_tokens;
     const int t1 = ONE ? p.T : min(p.T, t0 + p.block_tokens);
@@ -352,26 +433,26 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
             __syncthreads();
         }
     }
-    if constexpr (VPL > 0) {
-        constexpr int TOK = ROUTE_TOK<VPL>;
-        for (int t = t0 + wave; t < t1; t += RT_WAVES * TOK) {
-            int id[TOK];
-            float w[TOK];
-            route_tokens<VPL, BF16, TOK>(p, t, t1, lane, id, w);
-#pragma unroll
-            for (int q = 0; q < TOK; ++q) {
-                const int tq = t + q * RT_WAVES;
-                if (lane < p.k && tq < t1) {
-                    const int flat = tq * p.k + lane;
-                    p.ids[flat] = id[q];
-                    p.weights[flat] = w[q];
-                    if (group) {
-                        const int g = id[q] < 0 ? p.E : id[q];
-                        if (ONE)
-                            s_id[flat] = g;
-                        else
-                            atomicAdd(&l.total[g], 1);
-                    }
+    if constexpr (V > 0) {
+        constexpr int PER = RT_THREADS / LPT;            // tokens at a time
+        const int j = tid % LPT;
+        for (int tb = t0; tb < t1; tb += PER) {
+            const int t = tb + tid / LPT;
+            if (tb + wave * (64 / LPT) >= t1)
+                break;                                   // no token in this wave
+            int id;
+            float w;
+            route_token<LPT, V, BF16>(p, min(t, t1 - 1), j, id, w);
+            if (j < p.k && t < t1) {
+                const int flat = t * p.k + j;
+                p.ids[flat] = id;
+                p.weights[flat] = w;
+                if (group) {
+                    const int g = id < 0 ? p.E : id;
+                    if (ONE)
+                        s_id[flat] = g;
+                    else
+                        atomicAdd(&l.total[g], 1);
                 }
             }
         }
