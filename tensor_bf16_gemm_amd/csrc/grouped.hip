@@ -109,7 +109,7 @@ int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, ui
     const int64_t per = std::max<int64_t>({1, 512 / a.k, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS});
     const int blocks = (int)((a.T + per - 1) / per);
     a.block_tokens = (int)per;
-    a.cstride = (a.E + 1 + 7) / 8 * 8;
+    a.cstride = (a.E + 7) / 8 * 8;
     if (a.offsets) {
         if (!good16(workspace) || bytes < (uint64_t)(kCountBytes + (int64_t)blocks * a.cstride * 2))
             return GC_EINVAL;

@@ -9,14 +9,13 @@
 //
 // A token is a row of 16 lanes (four tokens per wave) for up to 256 experts,
 // else a whole wave; each lane holds V consecutive experts.  A (key, index)
-// pair is packed into the mantissa of a double in [1, 2) -- 32 bits of an
-// order-preserving key, then the index counted downwards -- so that one
-// v_max_f64 compares both and no two are equal.  Every lane sorts its V pairs
-// once (a network of min/max); a round of the choice is then a maximum over
-// the lanes' heads (four row rotations) and the winner's lane moves its list
-// up by one.  About 120 instructions per token at E = 256, k = 8, where the
-// rounds of a whole wave per token took 560 and the issue rate bound them
-// (16384 tokens: 16.8 us; this way LATER).
+// pair is packed into one number -- an order-preserving key, then the index
+// counted downwards -- so that one maximum compares both and no two are
+// equal: 16 + 16 bits of a word for bf16 logits, else 32 + 20 bits of the
+// mantissa of a double in [1, 2).  Every lane sorts its V pairs once (a
+// network of min/max); a round of the choice is then a maximum over the
+// lanes' heads (four row rotations) and the winner's lane moves its list up
+// by one.  The issue rate bounds it: MEASURED
 //
 // Grouping: a stable counting sort by blocks of consecutive items.  Counts
 // per block first (LDS integer atomics: order does not matter to a sum), then
@@ -57,7 +56,7 @@ struct RouteArgs {
     int32_t *rows;           // [T * k]
     int32_t *slots;          // [T * k]
     uint16_t *counts;        // [blocks][cstride]
-    int cstride;             // E + 1 rounded up to 8
+    int cstride;             // E rounded up to 8
     int block_tokens;        // tokens (items / k) per block
     bool vec;                // a lane's VPL logits are whole aligned vectors
 };
@@ -68,17 +67,32 @@ __device__ __forceinline__ uint32_t row_ror(uint32_t v)
 {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x120 + ROR, 0xf, 0xf, true);
 }
-
-// Maximum over the LPT lanes of a token (a row of 16, or the wave), in all of
-// them; the pairs are never NaN.
 template <int ROR>
-__device__ __forceinline__ double ror_max(double v)
+__device__ __forceinline__ double row_ror(double v)
 {
     const uint64_t b = (uint64_t)__double_as_longlong(v);
     const uint64_t o = ((uint64_t)row_ror<ROR>((uint32_t)(b >> 32)) << 32) | row_ror<ROR>((uint32_t)b);
-    return fmax(v, __longlong_as_double((long long)o));
+    return __longlong_as_double((long long)o);
 }
-// (the two halves of a swap with itself: the rows, or the wave halves, side by side)
+
+// (pairs are never NaN)
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b) { return a < b ? a : b; }
+__device__ __forceinline__ double pair_max(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double pair_min(double a, double b) { return fmin(a, b); }
+
+// Maximum of v and its partner's: the neighbouring row of 16, or (HALVES) the
+// other half of the wave (both halves of a swap with itself).
+template <bool HALVES>
+__device__ __forceinline__ uint32_t swap_max(uint32_t v)
+{
+    if (HALVES) {
+        const auto s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return pair_max((uint32_t)s[0], (uint32_t)s[1]);
+    }
+    const auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return pair_max((uint32_t)s[0], (uint32_t)s[1]);
+}
 template <bool HALVES>
 __device__ __forceinline__ double swap_max(double v)
 {
@@ -96,15 +110,17 @@ __device__ __forceinline__ double swap_max(double v)
         x = ((uint64_t)h[0] << 32) | l[0];
         y = ((uint64_t)h[1] << 32) | l[1];
     }
-    return fmax(__longlong_as_double((long long)x), __longlong_as_double((long long)y));
+    return pair_max(__longlong_as_double((long long)x), __longlong_as_double((long long)y));
 }
-template <int LPT>
-__device__ __forceinline__ double token_max(double v)
+// Maximum over the LPT lanes of a token (a row of 16, or the wave), in all of
+// them.
+template <int LPT, class P>
+__device__ __forceinline__ P token_max(P v)
 {
-    v = ror_max<8>(v);
-    v = ror_max<4>(v);
-    v = ror_max<2>(v);
-    v = ror_max<1>(v);
+    v = pair_max(v, row_ror<8>(v));
+    v = pair_max(v, row_ror<4>(v));
+    v = pair_max(v, row_ror<2>(v));
+    v = pair_max(v, row_ror<1>(v));
     if (LPT == 64) {
         v = swap_max<false>(v);
         v = swap_max<true>(v);
@@ -168,23 +184,54 @@ __device__ __forceinline__ float soft_term(float x, float high)
 
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// The pair of an expert as a double in [1, 2); NO_PAIR, the least, for an
-// expert that cannot be chosen.
-constexpr uint64_t PAIR_ONE = 0x3FF0000000000000ull;
-__device__ __forceinline__ double make_pair(uint32_t key, int e)
-{
-    const uint64_t b = key > KEY_NEG_INF ? PAIR_ONE | ((uint64_t)key << 20) | (uint32_t)(RT_GROUPS - 1 - e)
-                                         : PAIR_ONE;
-    return __longlong_as_double((long long)b);
-}
-__device__ __forceinline__ uint32_t pair_key(double v)
-{
-    return (uint32_t)((uint64_t)__double_as_longlong(v) >> 20);
-}
-__device__ __forceinline__ int pair_expert(double v)
-{
-    return RT_GROUPS - 1 - (int)((uint64_t)__double_as_longlong(v) & 0xFFFFFu);
-}
+// The pair of an expert; none() is the least, for one that cannot be chosen.
+// Wide: any key.  Narrow: the key of a bf16 value (its low 16 bits say nothing).
+struct WidePair {
+    using P = double;
+    static constexpr uint64_t ONE = 0x3FF0000000000000ull;
+    static __device__ __forceinline__ P none() { return __longlong_as_double((long long)ONE); }
+    static __device__ __forceinline__ P make(uint32_t key, int e)
+    {
+        const uint64_t b =
+            key > KEY_NEG_INF ? ONE | ((uint64_t)key << 20) | (uint32_t)(RT_GROUPS - 1 - e) : ONE;
+        return __longlong_as_double((long long)b);
+    }
+    static __device__ __forceinline__ uint32_t key(P v)
+    {
+        return (uint32_t)((uint64_t)__double_as_longlong(v) >> 20);
+    }
+    static __device__ __forceinline__ int expert(P v)
+    {
+        return RT_GROUPS - 1 - (int)((uint64_t)__double_as_longlong(v) & 0xFFFFFu);
+    }
+    // mask ? x : y by bits.  (A conditional between neighbours of an array in
+    // registers is turned into an index and a chain of compares.)
+    static __device__ __forceinline__ P pick(bool c, P x, P y)
+    {
+        const uint64_t mask = c ? ~0ull : 0ull;
+        const uint64_t a = (uint64_t)__double_as_longlong(x), b = (uint64_t)__double_as_longlong(y);
+        return __longlong_as_double((long long)((a & mask) | (b & ~mask)));
+    }
+};
+struct NarrowPair {
+    using P = uint32_t;
+    static __device__ __forceinline__ P none() { return 0u; }
+    static __device__ __forceinline__ P make(uint32_t key, int e)
+    {
+        return key > KEY_NEG_INF ? (key & 0xFFFF0000u) | (uint32_t)(RT_GROUPS - 1 - e) : 0u;
+    }
+    // (a negative value's key has ones in its low half)
+    static __device__ __forceinline__ uint32_t key(P v)
+    {
+        return v == 0u ? 0u : (v & 0x80000000u) ? v & 0xFFFF0000u : v | 0xFFFFu;
+    }
+    static __device__ __forceinline__ int expert(P v) { return RT_GROUPS - 1 - (int)(v & 0xFFFFu); }
+    static __device__ __forceinline__ P pick(bool c, P x, P y)
+    {
+        const uint32_t mask = c ? ~0u : 0u;
+        return (x & mask) | (y & ~mask);
+    }
+};
 
 // Odd-even merge network (Batcher) for V a power of two: its comparators, as
 // a table the compiler unrolls.
@@ -216,12 +263,12 @@ struct MergeNetwork {
     }
 };
 
-template <int V, int... I>
-__device__ __forceinline__ void sort_steps(double (&a)[V], std::integer_sequence<int, I...>)
+template <int V, class P, int... I>
+__device__ __forceinline__ void sort_steps(P (&a)[V], std::integer_sequence<int, I...>)
 {
     auto step = [&](auto c) {
         constexpr auto at = MergeNetwork<V>::pair(decltype(c)::value);
-        const double hi = fmax(a[at.lo], a[at.hi]), lo = fmin(a[at.lo], a[at.hi]);
+        const P hi = pair_max(a[at.lo], a[at.hi]), lo = pair_min(a[at.lo], a[at.hi]);
         a[at.lo] = hi;
         a[at.hi] = lo;
     };
@@ -229,19 +276,11 @@ __device__ __forceinline__ void sort_steps(double (&a)[V], std::integer_sequence
 }
 
 // Falling order.
-template <int V>
-__device__ __forceinline__ void sort_pairs(double (&a)[V])
+template <int V, class P>
+__device__ __forceinline__ void sort_pairs(P (&a)[V])
 {
     if constexpr (V > 1)
         sort_steps(a, std::make_integer_sequence<int, MergeNetwork<V>::count()>{});
-}
-
-// mask ? x : y by bits.  (A conditional between neighbours of an array in
-// registers is turned into an index and a chain of compares.)
-__device__ __forceinline__ double pick(uint64_t mask, double x, double y)
-{
-    const uint64_t a = (uint64_t)__double_as_longlong(x), b = (uint64_t)__double_as_longlong(y);
-    return __longlong_as_double((long long)((a & mask) | (b & ~mask)));
 }
 
 template <bool BF16>
@@ -255,7 +294,7 @@ __device__ __forceinline__ float logit(const RouteArgs &p, int t, int e)
 // Routes one token per LPT lanes.  Lane j < k of the token returns with the
 // j-th choice's expert (-1: none) in `id` and its weight in `w`.  `t` is the
 // lane's token, which must exist.
-template <int LPT, int V, bool BF16>
+template <int LPT, int V, bool BF16, class Pair>
 __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, int &id, float &w)
 {
     const int e0 = j * V;
@@ -278,54 +317,53 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, in
         for (int i = 0; i < V; ++i)
             x[i] = e0 + i < p.E ? logit<BF16>(p, t, e0 + i) : -__builtin_huge_valf();
     }
-    double a[V];
+    typename Pair::P a[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        a[i] = make_pair(order_key(x[i]), e0 + i);
+        a[i] = Pair::make(order_key(x[i]), e0 + i);
     // For a softmax over all experts: its maximum and its sum.
     float high = 0.f, total = 1.f;
     if (soft && (p.bias || !p.renorm)) {
-        double m = a[0];
+        auto m = a[0];
 #pragma unroll
         for (int i = 1; i < V; ++i)
-            m = fmax(m, a[i]);
-        high = key_value(pair_key(token_max<LPT>(m)));
+            m = pair_max(m, a[i]);
+        high = key_value(Pair::key(token_max<LPT>(m)));
         float part = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            part += pair_key(a[i]) != 0 ? soft_term(x[i], high) : 0.f;
+            part += a[i] != Pair::none() ? soft_term(x[i], high) : 0.f;
         total = token_sum<LPT>(part);
     }
     if (p.bias) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            if (pair_key(a[i]) != 0) {
+            if (a[i] != Pair::none()) {
                 const float s = soft ? soft_term(x[i], high) / total : sigmoid(x[i]);
-                a[i] = make_pair(order_key(s + p.bias[e0 + i]), e0 + i);
+                a[i] = Pair::make(order_key(s + p.bias[e0 + i]), e0 + i);
             }
     }
     sort_pairs(a);
-    const double none = __longlong_as_double((long long)PAIR_ONE);
-    double mine = none, best = none;
+    const auto none = Pair::none();
+    auto mine = none, best = none;
     for (int r = 0; r < p.k; ++r) {
-        const double top = token_max<LPT>(a[0]);
+        const auto top = token_max<LPT>(a[0]);
         if (r == 0)
             best = top;
-        mine = j == r ? top : mine;
+        mine = Pair::pick(j == r, top, mine);
         const bool won = a[0] == top;            // (none: its list is empty, moving it changes nothing)
-        const uint64_t mask = won ? ~0ull : 0ull;
 #pragma unroll
         for (int i = 0; i + 1 < V; ++i)
-            a[i] = pick(mask, a[i + 1], a[i]);
-        a[V - 1] = pick(mask, none, a[V - 1]);
+            a[i] = Pair::pick(won, a[i + 1], a[i]);
+        a[V - 1] = Pair::pick(won, none, a[V - 1]);
     }
-    const bool chosen = pair_key(mine) != 0;
-    id = chosen ? pair_expert(mine) : -1;
-    float val = key_value(pair_key(mine));
+    const bool chosen = mine != none;
+    id = chosen ? Pair::expert(mine) : -1;
+    float val = key_value(Pair::key(mine));
     if (p.bias)
         val = logit<BF16>(p, t, chosen ? id : 0);
     else if (soft && p.renorm)
-        high = key_value(pair_key(best));
+        high = key_value(Pair::key(best));
     w = !chosen ? 0.f : soft ? soft_term(val, high) : sigmoid(val);
     if (p.renorm)
         total = token_sum<LPT>(w);
@@ -340,6 +378,7 @@ struct GroupLds {
     int total[RT_GROUPS + 8];
     int wave_at[RT_WAVES][RT_GROUPS + 1];    // a pass: counts, then positions, per wave
     int wave_sum[RT_WAVES];
+    int grouped_before, none;                // items before the block in a group; next position of those in none
 };
 
 // Exclusive prefix sum of v over threads 0 .. RT_THREADS - 1, and the whole
@@ -389,10 +428,15 @@ __device__ __forceinline__ int rank_in_wave(GroupLds &l, bool live, int g, int g
 // Counts of group e in the waves to positions from `at` on; returns the next.
 __device__ __forceinline__ int counts_to_positions(GroupLds &l, int waves, int e, int at)
 {
-    for (int w = 0; w < waves; ++w) {
-        const int c = l.wave_at[w][e];
-        l.wave_at[w][e] = at;
-        at += c;
+    int c[RT_WAVES];                                     // (all read before any is written)
+#pragma unroll
+    for (int w = 0; w < RT_WAVES; ++w)
+        c[w] = w < waves ? l.wave_at[w][e] : 0;
+#pragma unroll
+    for (int w = 0; w < RT_WAVES; ++w) {
+        if (w < waves)
+            l.wave_at[w][e] = at;
+        at += c[w];
     }
     return at;
 }
@@ -442,7 +486,10 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
                 break;                                   // no token in this wave
             int id;
             float w;
-            route_token<LPT, V, BF16>(p, min(t, t1 - 1), j, id, w);
+            if (BF16 && !p.bias)
+                route_token<LPT, V, BF16, NarrowPair>(p, min(t, t1 - 1), j, id, w);
+            else
+                route_token<LPT, V, BF16, WidePair>(p, min(t, t1 - 1), j, id, w);
             if (j < p.k && t < t1) {
                 const int flat = t * p.k + j;
                 p.ids[flat] = id;
@@ -474,9 +521,11 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
         const int rank = rank_in_wave(l, live, g, p.E);
         __syncthreads();
         int sum = 0, all;
-        if (tid < p.E)
-            for (int w = 0; w < waves; ++w)
-                sum += l.wave_at[w][tid];
+        if (tid < p.E) {
+#pragma unroll
+            for (int w = 0; w < RT_WAVES; ++w)
+                sum += w < waves ? l.wave_at[w][tid] : 0;
+        }
         const int at = block_scan(l, sum, all);
         if (tid < p.E) {
             counts_to_positions(l, waves, tid, at);
@@ -491,7 +540,7 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
             place(p, tid, g, l.wave_at[wave][g] + rank);
     } else {
         for (int e = tid; e < p.cstride; e += RT_THREADS)
-            p.counts[(int64_t)blockIdx.x * p.cstride + e] = e <= p.E ? (uint16_t)l.total[e] : (uint16_t)0;
+            p.counts[(int64_t)blockIdx.x * p.cstride + e] = e < p.E ? (uint16_t)l.total[e] : (uint16_t)0;
     }
 }
 
@@ -505,6 +554,12 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
         l.base[e] = 0;
         l.total[e] = 0;
     }
+    if (tid == 0)
+        l.grouped_before = 0;
+    const int first = b * p.block_tokens * p.k;
+    const int n = (min(p.T, (b + 1) * p.block_tokens) - b * p.block_tokens) * p.k;
+    auto group_at = [&](int i) { return i < n ? group_of(p.ids[first + i], p.E) : 0; };
+    int g = group_at(tid);                               // (asked for before the counts)
     __syncthreads();
     // Counts of the blocks before this one (base) and of all (total): a
     // thread adds 8 neighbouring groups over every per_pass-th block.  In the
@@ -512,24 +567,39 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
     // addition, whose c differ, fall into different banks.
     const int lanes = p.cstride / 8, per_pass = RT_THREADS / lanes;
     const int r0 = tid / lanes, c = tid - r0 * lanes;
+    int before = 0;
     if (r0 < per_pass) {
+        constexpr int AHEAD = 8;                         // rows asked for at once
         int pre[8] = {}, tot[8] = {};
-#pragma unroll 4
-        for (int r = r0; r < blocks; r += per_pass) {
-            const u32x4_t v = *(const u32x4_t *)(p.counts + (int64_t)r * p.cstride + 8 * c);
+        for (int q = r0; q < blocks; q += AHEAD * per_pass) {
+            u32x4_t v[AHEAD];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int n = (int)((v[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                tot[i] += n;
-                pre[i] += r < b ? n : 0;
+            for (int d = 0; d < AHEAD; ++d) {
+                const int r = q + d * per_pass;
+                v[d] = *(const u32x4_t *)(p.counts + (int64_t)min(r, blocks - 1) * p.cstride + 8 * c);
+            }
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d) {
+                const int r = q + d * per_pass;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int n = (int)((v[d][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+                    tot[i] += r < blocks ? n : 0;
+                    pre[i] += r < b ? n : 0;
+                }
             }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             atomicAdd(&l.total[i * lanes + c], tot[i]);
             atomicAdd(&l.base[i * lanes + c], pre[i]);
+            before += pre[i];
         }
     }
+    // What the blocks before have in no group is the rest of their items.
+    before = wave_scan(before);
+    if ((tid & 63) == 63)
+        atomicAdd(&l.grouped_before, before);
     __syncthreads();
     auto kept = [&](int e) { return (e & 7) * lanes + (e >> 3); };
     int all;
@@ -539,23 +609,24 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
         if (b == 0)
             p.offsets[tid] = at;
     }
-    if (tid == 0) {
-        l.base[kept(p.E)] += all;
+    if (tid == RT_THREADS - 1) {
+        l.none = all + first - l.grouped_before;
         if (b == 0)
             p.offsets[p.E] = all;
     }
-    const int first = b * p.block_tokens * p.k;
-    const int n = (min(p.T, (b + 1) * p.block_tokens) - b * p.block_tokens) * p.k;
     for (int i0 = 0; i0 < n; i0 += RT_THREADS) {
         const int waves = min(RT_WAVES, (n - i0 + 63) / 64);
         clear_wave_at(l, waves, p.E);
         const bool live = i0 + tid < n;
-        const int g = live ? group_of(p.ids[first + i0 + tid], p.E) : 0;
+        if (i0 > 0)
+            g = group_at(i0 + tid);
         __syncthreads();
         const int rank = rank_in_wave(l, live, g, p.E);
         __syncthreads();
-        for (int e = tid; e <= p.E; e += RT_THREADS)
-            l.base[kept(e)] = counts_to_positions(l, waves, e, l.base[kept(e)]);
+        if (tid < p.E)
+            l.base[kept(tid)] = counts_to_positions(l, waves, tid, l.base[kept(tid)]);
+        if (tid == RT_THREADS - 1)
+            l.none = counts_to_positions(l, waves, p.E, l.none);
         __syncthreads();
         if (live)
             place(p, first + i0 + tid, g, l.wave_at[wave][g] + rank);
