@@ -58,26 +58,19 @@ __device__ __forceinline__ void group_range(const int32_t *offsets, int E, int S
     hi = e < E ? min(max(offsets[e + 1], lo), S) : S;
 }
 
-// first[e] = tiles of the groups before e, e = 0 .. groups, for tiles of `bm`
-// positions and tiles_n columns tiles; returns the number of tiles.
-// NTH threads; groups (E, or E + 1 with the positions past the last) <= 1024.
-template <int NTH>
-__device__ __forceinline__ int scan_tiles(const int32_t *offsets, int E, int S, int groups, int bm,
-                                          int tiles_n, int *first, int *wsum)
+// first[i] = the sum of count(0 .. i - 1), i = 0 .. n; returns the whole sum.
+// NTH threads; n <= 1024.
+template <int NTH, class F>
+__device__ __forceinline__ int scan_counts(int n, F &&count, int *first, int *wsum)
 {
     constexpr int PER = GR_GROUPS / NTH;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    int n[PER], sum = 0;
+    int c[PER], sum = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = PER * tid + i;
-        n[i] = 0;
-        if (e < groups) {
-            int lo, hi;
-            group_range(offsets, E, S, e, lo, hi);
-            n[i] = (hi - lo + bm - 1) / bm * tiles_n;
-        }
-        sum += n[i];
+        const int at = PER * tid + i;
+        c[i] = at < n ? count(at) : 0;
+        sum += c[i];
     }
     int inc = sum;
 #pragma unroll
@@ -97,15 +90,29 @@ __device__ __forceinline__ int scan_tiles(const int32_t *offsets, int E, int S, 
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int e = PER * tid + i;
-        if (e < groups)
-            first[e] = at;
-        at += n[i];
+        if (PER * tid + i < n)
+            first[PER * tid + i] = at;
+        at += c[i];
     }
     if (tid == 0)
-        first[groups] = all;
+        first[n] = all;
     __syncthreads();
     return __builtin_amdgcn_readfirstlane(all);
+}
+
+// first[e] = tiles of the groups before e, for tiles of `bm` positions and
+// tiles_n columns tiles; returns the number of tiles.  groups: E, or E + 1
+// with the positions past the last.
+template <int NTH>
+__device__ __forceinline__ int scan_tiles(const int32_t *offsets, int E, int S, int groups, int bm,
+                                          int tiles_n, int *first, int *wsum)
+{
+    auto count = [&](int e) {
+        int lo, hi;
+        group_range(offsets, E, S, e, lo, hi);
+        return (hi - lo + bm - 1) / bm * tiles_n;
+    };
+    return scan_counts<NTH>(groups, count, first, wsum);
 }
 
 // Group of tile t: the last e with first[e] <= t (two looks of a whole wave).
