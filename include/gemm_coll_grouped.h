@@ -30,10 +30,10 @@
  *   rows     int32 [n]: row of the item at each position (items in no group
  *            come last, after offsets[groups], in their order)
  *   slots    int32 [n]: position of each item, -1 for an item in no group
- * Groups keep the order of their items.  Kernels read offsets and rows on
- * the device and stay in bounds whatever they hold: an offset is clamped to
- * [0, S], a row outside its matrix reads as zeros (and is not written by
- * lora_add).
+ * Groups keep the order of their items.  offsets do not fall.  Kernels read
+ * offsets and rows on the device and stay in bounds whatever they hold: an
+ * offset is clamped to [0, S], a row outside its matrix reads as zeros (and is
+ * not written by lora_add).
  *
  * Workspace.  `workspace` points to workspace_bytes of device memory, zeroed
  * before its first use and not used by two calls at the same time; calls on
@@ -61,7 +61,7 @@ extern "C" {
 #define GC_ACT_SILU_GLU 1
 
 /* Bytes of workspace that every call here can be given on the current device
- * (about 16 MiB on MI355X; lora_add of many rows needs more); negative on a
+ * (64 MiB; lora_add of very many rows needs more); negative on a
  * HIP error. */
 int64_t gemm_coll_grouped_workspace_bytes(void);
 
@@ -109,6 +109,16 @@ int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32
 int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const int32_t *offsets,
                            const int32_t *rows, int64_t S, int64_t K, int64_t N, int E, int act,
                            gc_bf16 *out, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* How gemm_coll_grouped_gemm runs these sizes on a device of `cus` compute
+ * units (host arithmetic only; GC_EINVAL for sizes it would refuse). */
+typedef struct gc_grouped_plan {
+    int32_t tiles;       /* 1: 256-column tiles of up to 256 rows; 0: streaming tiles of 128 columns */
+    int32_t splits;      /* tiles: pieces of K, summed by a second launch (1: none) */
+    int32_t block_rows;  /* streaming: rows of a tile, 16, 32 or 64 */
+} gc_grouped_plan;
+int gemm_coll_grouped_plan(int64_t S, int64_t K, int64_t N, int E, int act, int with_workspace, int cus,
+                           gc_grouped_plan *plan);
 
 /*
  * Combine.  out[t] = bf16( sum_j weights[t][j] * Y[slots[t][j]]

@@ -389,7 +389,7 @@ def ag_push_shards(src, dst, flags, epoch_word, *, R: int, rank: int, stream=Non
 
 
 _GROUPED = ("moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add", "Routing", "Groups",
-            "grouped_workspace_bytes", "lora_workspace_bytes")
+            "grouped_plan", "grouped_workspace_bytes", "lora_workspace_bytes")
 
 
 def __getattr__(name):

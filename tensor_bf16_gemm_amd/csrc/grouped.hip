@@ -47,16 +47,17 @@ bool good4(const void *p) { return p && aligned(p, 4); }
 // sentinel at 2^31.
 bool fits(int64_t rows, int64_t cols) { return cols == 0 || rows < ((int64_t)1 << 30) / cols; }
 
-// Workspace: counters (4 KiB, zero between launches), then partial tiles of
-// the streaming kernel, two of at most kPartBytes per workgroup.  The
-// many-block grouping keeps its counts where the partial tiles are, and
-// lora_add its middle sums.
+// Workspace: counters (4 KiB, zero between launches), then room for one of
+// the partial tiles of the streaming kernel (two of at most kPartBytes per
+// workgroup), the fp32 sums of products split along K, the counts of a
+// many-block grouping, or lora_add's middle sums.
 constexpr int64_t kCountBytes = 4096;
 constexpr int64_t kPartBytes = 32768;
+constexpr int64_t kSumBytes = (int64_t)64 << 20;
 constexpr int kMaxWorkers = (int)(kCountBytes / 4);
 
 int workers(int cus) { return std::min(cus, kMaxWorkers); }
-int64_t base_bytes(int cus) { return kCountBytes + 2 * kPartBytes * workers(cus); }
+int64_t base_bytes(int cus) { return kCountBytes + std::max(kSumBytes, 2 * kPartBytes * workers(cus)); }
 
 int launched() { return hipGetLastError() == hipSuccess ? GC_OK : GC_EIO; }
 
@@ -140,15 +141,14 @@ void launch_stream(gc::GroupedArgs &a, int cus, hipStream_t st)
     hipLaunchKernelGGL((gc::stream_kernel<NB, RB, D, EPI>), dim3(grid), dim3(gc::ST_THREADS), 0, st, a);
 }
 
-template <int NB, int EPI>
-void launch_stream_rows(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hipStream_t st)
+template <int EPI>
+void launch_stream_rows(gc::GroupedArgs &a, int blocks, int cus, hipStream_t st)
 {
-    if (rows_per_group <= 16)
-        launch_stream<NB, 1, 4, EPI>(a, cus, st);
-    else if (rows_per_group <= 32)
-        launch_stream<NB, 2, 3, EPI>(a, cus, st);
-    else
-        launch_stream<NB, 4, 3, EPI>(a, cus, st);
+    switch (blocks) {
+    case 1: launch_stream<8, 1, 4, EPI>(a, cus, st); break;
+    case 2: launch_stream<8, 2, 3, EPI>(a, cus, st); break;
+    default: launch_stream<8, 4, 3, EPI>(a, cus, st); break;
+    }
 }
 
 // Middle sums of the adapters: tiles of 16, 32 or 64 rows, K cut into so many
@@ -160,7 +160,7 @@ void launch_sums_rows(gc::GroupedArgs &a, int cus, hipStream_t st)
 {
     const int bm = 16 * RB, kt = (a.K + gc::BK - 1) / gc::BK;
     const int64_t most = std::min<int64_t>(a.S, (int64_t)(a.S + bm - 1) / bm + a.E);
-    const int64_t about = std::min<int64_t>(a.S, (int64_t)a.S / bm + (a.E + 1) / 2);
+    const int64_t about = std::min<int64_t>(a.S, (int64_t)a.S / bm + (RB == 4 ? (a.E + 1) / 2 : a.E));
     a.tiles_n = 1;
     a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, (cus + about / 2) / about, kt / 8}));
     const int grid = (int)std::min<int64_t>(most * a.splits, 4 * cus);
@@ -178,11 +178,66 @@ void launch_sums(gc::GroupedArgs &a, int64_t rows_per_group, int cus, hipStream_
         launch_sums_rows<NB, 4, NB == 8 ? 3 : 4>(a, cus, st);
 }
 
-template <bool GLU>
-void launch_tiles(gc::GroupedArgs &a, int cus, hipStream_t st)
+// How a grouped product is run.
+struct GroupedPlan {
+    bool tiles;      // tile_kernel, else stream_kernel
+    int splits;      // tile_kernel: pieces of K
+    int blocks;      // stream_kernel: blocks of 16 rows in a tile
+};
+
+// The cheapest by three estimates in us, fitted to measurements at K = 512 to
+// 7168, N = 512 to 7168, 4 to 64 groups of 1 to 1024 rows:
+//   stream   every ceil(rows / tile rows) pass reads the weights at 5.3 TB/s,
+//            and 8 us
+//   tiles    rounds of tiles (one at least) of 0.6 us a K-step, 0.93 with 256
+//            rows; the weights at 6.3 TB/s at best; and 12 us
+//   split    the pieces' rounds the same but 15 % slower, 22 us, and the sums
+//            written and read at 4 TB/s; where the sums have room
+// (us measured, stream / tiles / split: K 7168, N 1792, 64 groups of 16 rows
+// 282 / 272 / -; 8 groups of 8 rows 38 / 163 / 57, of 64 rows 48 / 175 / 77,
+// of 192 rows 122 / 213 / 123, of 256 rows 163 / 225 / 140.)  Groups are taken
+// as equally large, as many as there are rows at most; a stream tile has room
+// for twice the average rows, for real groups are not equal.
+GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool glu, bool workspace, int cus)
 {
-    a.tiles_n = GLU ? (a.N / 2 + gc::BN / 2 - 1) / (gc::BN / 2) : (a.N + gc::BN - 1) / gc::BN;
-    hipLaunchKernelGGL((gc::tile_kernel<GLU>), dim3(cus), dim3(gc::NT), 0, st, a);
+    GroupedPlan pl = {};
+    const int64_t used = std::min<int64_t>(E, S), rows = (S + used - 1) / used;
+    const int kt = (int)((K + gc::BK - 1) / gc::BK);
+    const double w = (double)used * K * N * 2e-6;                       // MB of weights
+    pl.blocks = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+    const double t_stream = (double)((rows + 16 * pl.blocks - 1) / (16 * pl.blocks)) * w / 5.3 + 8;
+    const int64_t bn = glu ? gc::BN / 2 : gc::BN, tiles_n = (F + bn - 1) / bn;
+    const double tiles = (double)used * std::max(1.0, (double)rows / 256 + 0.5) * tiles_n;
+    const double step = 0.6 + 0.0013 * std::min<int64_t>(rows, 256);
+    pl.splits = 1;
+    double best = 12 + std::max(std::max(1.0, tiles / cus) * kt * step, w / 6.3);
+    for (int q = 2; workspace && q <= 8 && kt / q >= 16 && q * S * N * 4 <= kSumBytes; ++q) {
+        const double t = 22 + std::max(1.15 * std::max(1.0, q * tiles / cus) * ((kt + q - 1) / q) * step, w / 6.3) +
+                         (double)q * S * N * 8e-6 / 4.0;
+        if (t < best) {
+            best = t;
+            pl.splits = q;
+        }
+    }
+    pl.tiles = best < t_stream;
+    return pl;
+}
+
+template <bool GLU>
+void launch_tiles(gc::GroupedArgs &a, int splits, int cus, hipStream_t st)
+{
+    const int f = GLU ? a.N / 2 : a.N, bn = GLU ? gc::BN / 2 : gc::BN;
+    a.tiles_n = (f + bn - 1) / bn;
+    a.splits = splits;
+    if (splits == 1) {
+        hipLaunchKernelGGL((gc::tile_kernel<GLU, false>), dim3(cus), dim3(gc::NT), 0, st, a);
+        return;
+    }
+    a.sums = a.part;
+    hipLaunchKernelGGL((gc::tile_kernel<GLU, true>), dim3(cus), dim3(gc::NT), 0, st, a);
+    const int64_t vecs = (int64_t)a.S * f / 8;
+    const int grid = (int)std::min<int64_t>((vecs + gc::FINISH_THREADS - 1) / gc::FINISH_THREADS, 8 * cus);
+    hipLaunchKernelGGL((gc::finish_kernel<GLU>), dim3(grid), dim3(gc::FINISH_THREADS), 0, st, a);
 }
 
 void launch_expand(gc::ExpandArgs &a, int cus, hipStream_t st)
@@ -348,17 +403,38 @@ int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const 
     a.K = (int)K;
     a.N = (int)N;
     a.E = E;
-    const int64_t avg = (S + E - 1) / E;
-    if (avg > 64) {
-        if (act == GC_ACT_SILU_GLU)
-            launch_tiles<true>(a, cus, (hipStream_t)stream);
-        else
-            launch_tiles<false>(a, cus, (hipStream_t)stream);
-    } else if (act == GC_ACT_SILU_GLU)
-        launch_stream_rows<8, gc::EPI_GLU>(a, avg, cus, (hipStream_t)stream);
+    const bool glu = act == GC_ACT_SILU_GLU;
+    const hipStream_t st = (hipStream_t)stream;
+    const GroupedPlan pl = plan_grouped(S, K, N, glu ? N / 2 : N, E, glu, workspace != nullptr, cus);
+    if (pl.tiles && glu)
+        launch_tiles<true>(a, pl.splits, cus, st);
+    else if (pl.tiles)
+        launch_tiles<false>(a, pl.splits, cus, st);
+    else if (glu)
+        launch_stream_rows<gc::EPI_GLU>(a, pl.blocks, cus, st);
     else
-        launch_stream_rows<8, gc::EPI_PLAIN>(a, avg, cus, (hipStream_t)stream);
+        launch_stream_rows<gc::EPI_PLAIN>(a, pl.blocks, cus, st);
     return launched();
+}
+
+int gemm_coll_grouped_plan(int64_t S, int64_t K, int64_t N, int E, int act, int with_workspace, int cus,
+                           gc_grouped_plan *plan)
+{
+    if (!plan || S < 0 || K < 0 || N < 0 || E < 1 || E > GC_GROUPS_MAX || cus < 1 || cus > 4096 ||
+        (act != GC_ACT_NONE && act != GC_ACT_SILU_GLU) || K % 8 != 0 ||
+        N % (act == GC_ACT_SILU_GLU ? 16 : 8) != 0)
+        return GC_EINVAL;
+    if (S > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX || !fits(K, N) || !fits(S, N))
+        return GC_ENOTSUP;
+    *plan = {};
+    if (S == 0 || N == 0)
+        return GC_OK;
+    const GroupedPlan pl = plan_grouped(S, K, N, act == GC_ACT_SILU_GLU ? N / 2 : N, E, act == GC_ACT_SILU_GLU,
+                                        with_workspace != 0, cus);
+    plan->tiles = pl.tiles;
+    plan->splits = pl.tiles ? pl.splits : 1;
+    plan->block_rows = pl.tiles ? 0 : 16 * pl.blocks;
+    return GC_OK;
 }
 
 int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, const float *weights,

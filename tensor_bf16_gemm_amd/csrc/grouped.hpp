@@ -37,7 +37,7 @@ struct GroupedArgs {
     const int32_t *offsets;    // [E + 1]
     const int32_t *rows;       // [S] or null
     uint16_t *out;             // PLAIN [S][N], GLU [S][N/2]
-    float *sums;               // SUMS [splits][S][N]
+    float *sums;               // sums over pieces of K [splits][S][N]
     int splits;
     int T, S, K, N, E;
     int tiles_n;               // column tiles

@@ -23,6 +23,11 @@
 // which its workgroups draw tickets (from the next where theirs is empty).
 // (32768 rows in 64 groups, 4 rounds of tiles: 811 us, against 845 in the
 // order of the groups, and 936 with all short tiles last, which read W twice.)
+//
+// Fewer tiles than CUs: K is cut into p.splits equal pieces, each unit (piece,
+// tile) leaves its fp32 sums in the workspace, and finish_kernel, a launch of
+// its own at the bandwidth of the whole chip, adds them in the order of K and
+// applies the end.  (8 groups of 256 rows, K 7168, N 1792: LATER)
 #pragma once
 
 #include "grouped.hpp"
@@ -36,10 +41,11 @@ constexpr int TK_TICKET_STRIDE = 16, TK_DONE = TK_QUEUES * TK_TICKET_STRIDE;
 
 struct TileAt {
     int e, lo, hi, m0, nt;
+    int piece, k_begin, steps;     // piece of K: `steps` steps from step k_begin on
 };
 
-// One tile of 32*FMT positions.
-template <int FMT, bool GLU>
+// One tile of 32*FMT positions.  SUMS: its fp32 sums go to p.sums.
+template <int FMT, bool GLU, bool SUMS>
 __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, const TileAt &at, int wave,
                                          int lane)
 {
@@ -48,7 +54,7 @@ __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, co
     const int fi = lane & 15, fg = lane >> 4;
     const int F = GLU ? p.N / 2 : p.N;
     const uint32_t N2 = (uint32_t)p.N * 2u;
-    const int KT = (p.K + BK - 1) / BK;
+    const int KT = at.steps;
     const u32x4_t rW = make_rsrc4(p.W + (size_t)at.e * p.K * p.N, (uint32_t)p.K * N2);
     const u32x4_t rX = make_rsrc4(p.X, (uint32_t)p.T * (uint32_t)p.K * 2u);
 
@@ -83,11 +89,12 @@ __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, co
     // Loads of step kt; past the K loop the same number of empty ones.  (An
     // offset of OOB plus a step's advance, below 2^31, is still out of range.)
     auto load = [&](int kt, uint32_t st) {
-        const int k0 = kt * BK;
+        const int k0 = (at.k_begin + kt) * BK;
+        const bool live = kt < KT;
         const uint32_t ka = (uint32_t)k0 * 2u, kb = (uint32_t)k0 * N2;
         const uint32_t la = st + (uint32_t)(2 * wave * 1024);
         const uint32_t lb = st + (uint32_t)(A_BYTES + 4 * wave * 512);
-        if (k0 + BK <= p.K) {
+        if (live && k0 + BK <= p.K) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 dma16(rX, la + j * 1024, a_off[j] + ka);
@@ -96,13 +103,13 @@ __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, co
                 dma16(rW, lb + j * 1024, b_off[j] + kb);
         } else {
             // (rows of W past K lie past its buffer)
-            const bool on = k0 + 8 * a_c < p.K;
+            const bool on = live && k0 + 8 * a_c < p.K;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 dma16(rX, la + j * 1024, on ? a_off[j] + ka : OOB);
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-                dma16(rW, lb + j * 1024, k0 < p.K ? b_off[j] + kb : OOB);
+                dma16(rW, lb + j * 1024, live && k0 < p.K ? b_off[j] + kb : OOB);
         }
     };
     const uint32_t a_frag = (uint32_t)(wm * WMt * 64 + fi * 64 + ((fg ^ ((fi >> 1) & 3)) << 4));
@@ -171,6 +178,25 @@ __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, co
     if (!lag)
         barrier_only();
 
+    if constexpr (SUMS) {
+        // 4 columns of a row per lane and block
+        const int ln = opaque_v(lane);
+        const int fi2 = ln & 15, fg2 = ln >> 4;
+#pragma unroll
+        for (int i = 0; i < FMT; ++i) {
+            const int m = at.m0 + wm * WMt + 16 * i + fi2;
+            float *row = p.sums + ((size_t)at.piece * p.S + m) * p.N;
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int h = GLU ? at.nt * (BN / 2) + 32 * wn + 16 * (j & 1) + 4 * fg2
+                                  : at.nt * BN + 64 * wn + 16 * j + 4 * fg2;
+                if (m < at.hi && h < F)
+                    *(f32x4_t *)(row + (GLU && j >= 2 ? F + h : h)) = acc[i][j];
+            }
+        }
+        return;
+    }
+
     // ---- epilogue: 16-byte stores of 8 columns per lane ----
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.S * (uint32_t)F * 2u);
     const int ln = opaque_v(lane);
@@ -195,7 +221,7 @@ __device__ __forceinline__ void run_tile(const GroupedArgs &p, uint32_t lds0, co
     }
 }
 
-template <bool GLU>
+template <bool GLU, bool SUMS>
 __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t stages[STAGES * (A_BYTES + B_BYTES)];
@@ -228,10 +254,14 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
         return (g.y - g.x + BM - 1) / BM * p.tiles_n;
     };
     const int tiles = scan_counts<NT>(p.E, count, first, wsum);
-    // Queue x holds hands x, x + 8, ... of TK_HAND tiles.
+    // Units: the tiles of the first piece of K, then those of the next.
+    const int splits = SUMS ? p.splits : 1;
+    const int KT = (p.K + BK - 1) / BK, piece_steps = (KT + splits - 1) / splits;
+    const int units = tiles * splits;
+    // Queue x holds hands x, x + 8, ... of TK_HAND units.
     int x = blockIdx.x & (TK_QUEUES - 1), tried = 0, mine = blockIdx.x / TK_QUEUES;
     const int per_queue = (G + TK_QUEUES - 1) / TK_QUEUES;
-    // Next tile for this workgroup, or -1 (thread 0 only).
+    // Next unit for this workgroup, or -1 (thread 0 only).
     auto draw = [&]() {
         for (; tried < TK_QUEUES; ++tried, x = (x + 1) & (TK_QUEUES - 1)) {
             int t;
@@ -245,7 +275,7 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
                 mine += per_queue;
             }
             t = (t / TK_HAND * TK_QUEUES + x) * TK_HAND + t % TK_HAND;
-            if (t < tiles)
+            if (t < units)
                 return t;
         }
         return -1;
@@ -255,13 +285,17 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
     const uint32_t lds0 = lds_addr(stages);
     for (;;) {
         __syncthreads();
-        const int t = __builtin_amdgcn_readfirstlane(s_next);
+        const int unit = __builtin_amdgcn_readfirstlane(s_next);
         __syncthreads();
-        if (t < 0)
+        if (unit < 0)
             break;
         if (tid == 0)
             s_next = draw();
         TileAt at;
+        at.piece = SUMS ? unit / max(tiles, 1) : 0;
+        at.k_begin = at.piece * piece_steps;
+        at.steps = max(min(piece_steps, KT - at.k_begin), 0);
+        const int t = unit - at.piece * tiles;
         const int rank = __builtin_amdgcn_readfirstlane(find_group(first, p.E, t, lane));
         at.e = __builtin_amdgcn_readfirstlane(order[rank]);
         at.lo = __builtin_amdgcn_readfirstlane(range[at.e].x);
@@ -274,14 +308,14 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
         at.nt = rest / max(high, 1);
         at.m0 = at.lo + (band * TK_GROUP_M + rest - at.nt * high) * BM;
         switch (min(8, (at.hi - at.m0 + 31) / 32)) {
-        case 1: run_tile<1, GLU>(p, lds0, at, wave, lane); break;
-        case 2: run_tile<2, GLU>(p, lds0, at, wave, lane); break;
-        case 3: run_tile<3, GLU>(p, lds0, at, wave, lane); break;
-        case 4: run_tile<4, GLU>(p, lds0, at, wave, lane); break;
-        case 5: run_tile<5, GLU>(p, lds0, at, wave, lane); break;
-        case 6: run_tile<6, GLU>(p, lds0, at, wave, lane); break;
-        case 7: run_tile<7, GLU>(p, lds0, at, wave, lane); break;
-        default: run_tile<8, GLU>(p, lds0, at, wave, lane); break;
+        case 1: run_tile<1, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 2: run_tile<2, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 3: run_tile<3, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 4: run_tile<4, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 5: run_tile<5, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 6: run_tile<6, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        case 7: run_tile<7, GLU, SUMS>(p, lds0, at, wave, lane); break;
+        default: run_tile<8, GLU, SUMS>(p, lds0, at, wave, lane); break;
         }
         wait_vmcnt<0>();                         // the stages are free for the next tile
     }
@@ -295,6 +329,34 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
                                    __HIP_MEMORY_SCOPE_AGENT);
             __hip_atomic_store(p.count + TK_DONE, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
+    }
+}
+
+// out = the end of the sums of every position in a group, 8 columns a thread.
+constexpr int FINISH_THREADS = 256;
+template <bool GLU>
+__global__ __launch_bounds__(FINISH_THREADS) void finish_kernel(GroupedArgs p)
+{
+    const int F = GLU ? p.N / 2 : p.N, vecs = F / 8;
+    const int lo = min(max(p.offsets[0], 0), p.S), hi = min(max(p.offsets[p.E], lo), p.S);
+    const int64_t n = (int64_t)(hi - lo) * vecs, step = (int64_t)gridDim.x * FINISH_THREADS;
+    const size_t plane = (size_t)p.S * p.N;
+    for (int64_t i = (int64_t)blockIdx.x * FINISH_THREADS + threadIdx.x; i < n; i += step) {
+        const int m = lo + (int)(i / vecs), c = (int)(i % vecs) * 8;
+        auto sum = [&](int col) {
+            const float *at = p.sums + (size_t)m * p.N + col;
+            f32x4_t x = *(const f32x4_t *)at;
+            for (int s = 1; s < p.splits; ++s)
+                x += *(const f32x4_t *)(at + s * plane);
+            return x;
+        };
+        f32x4_t x = sum(c), y = sum(c + 4);
+        if (GLU) {
+            x = silu_mul(x, sum(F + c));
+            y = silu_mul(y, sum(F + c + 4));
+        }
+        const u32x2_t a = pack_bf16x4(x), b = pack_bf16x4(y);
+        *(u32x4_t *)(p.out + (size_t)m * F + c) = (u32x4_t){a[0], a[1], b[0], b[1]};
     }
 }
 

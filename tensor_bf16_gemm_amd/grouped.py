@@ -34,7 +34,7 @@ except ImportError as e:
                        "`python -m tensor_bf16_gemm_amd.build`") from e
 
 __all__ = ["moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add", "Routing", "Groups",
-           "grouped_workspace_bytes", "lora_workspace_bytes"]
+           "grouped_plan", "grouped_workspace_bytes", "lora_workspace_bytes"]
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _ACTS = {None: 0, "silu_glu": 1}
@@ -56,6 +56,11 @@ class Groups(NamedTuple):
     slots: torch.Tensor
 
 
+class GroupedPlan(ctypes.Structure):
+    """Mirror of ``gc_grouped_plan`` in include/gemm_coll_grouped.h."""
+    _fields_ = [("tiles", ctypes.c_int32), ("splits", ctypes.c_int32), ("block_rows", ctypes.c_int32)]
+
+
 def declare(L: ctypes.CDLL) -> None:
     """Sets the signatures of the functions of include/gemm_coll_grouped.h."""
     i, i64, vp, u64 = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_uint64
@@ -66,6 +71,7 @@ def declare(L: ctypes.CDLL) -> None:
                                      vp, vp, u64, vp], i),
             ("gemm_coll_group_rows", [vp, i64, i, i, vp, vp, vp, vp, u64, vp], i),
             ("gemm_coll_grouped_gemm", [vp, i64, vp, vp, vp, i64, i64, i64, i, i, vp, vp, u64, vp], i),
+            ("gemm_coll_grouped_plan", [i64, i64, i64, i, i, i, i, ctypes.POINTER(GroupedPlan)], i),
             ("gemm_coll_moe_combine", [vp, i64, vp, vp, i64, i, i64, vp, i, i64, vp, vp], i),
             ("gemm_coll_lora_add", [vp, vp, vp, vp, vp, vp, vp, i64, i64, i64, i, i, vp, vp, u64, vp], i)):
         f = getattr(L, name)
@@ -88,6 +94,15 @@ def grouped_workspace_bytes() -> int:
             raise RuntimeError(f"gemm_coll_grouped_workspace_bytes: {_gc.strerror(n)}")
         _base_bytes[dev] = n
     return n
+
+
+def grouped_plan(S: int, K: int, N: int, E: int, *, act: str | None = None, workspace: bool = True,
+                 cus: int = 256) -> dict:
+    """How grouped_gemm runs S rows in E groups (host arithmetic only, no GPU needed)."""
+    pl = GroupedPlan()
+    rc = _gc.lib().gemm_coll_grouped_plan(S, K, N, E, _ACTS[act], int(workspace), cus, ctypes.byref(pl))
+    _gc._check(rc, "grouped_plan")
+    return {n: int(getattr(pl, n)) for n, _ in GroupedPlan._fields_}
 
 
 def lora_workspace_bytes(M: int, r: int) -> int:
@@ -184,4 +199,4 @@ def lora_add(base, X, down, up, scale, offsets, rows, out=None, *, stream=None, 
     for rows of no adapter.  down [G,K,r], up [G,r,N], scale float32 [G]; out may be base."""
     sums = X.shape[0] * down.shape[-1]               # fp32, in the workspace
     return _native.lora_add(base, X, down, up, scale, offsets, rows, out,
-                            *_place(X, workspace, 4 * sums if sums > 1 << 20 else 0, stream))
+                            *_place(X, workspace, 4 * sums if sums > 1 << 24 else 0, stream))

@@ -28,7 +28,7 @@ def test_exports_every_declared_function(L):
     names = set(re.findall(r"^\s*int(?:64_t)?\s+(gemm_coll_\w+)\s*\(", text, flags=re.M))
     assert names == {"gemm_coll_grouped_workspace_bytes", "gemm_coll_moe_route", "gemm_coll_group_rows",
                      "gemm_coll_grouped_gemm", "gemm_coll_moe_combine", "gemm_coll_lora_add",
-                     "gemm_coll_lora_workspace_bytes"}
+                     "gemm_coll_lora_workspace_bytes", "gemm_coll_grouped_plan"}
     out = subprocess.run(["nm", "-D", "--defined-only", gc.LIB_PATH], capture_output=True, text=True,
                          check=True).stdout
     assert names <= {l.split()[-1] for l in out.splitlines() if " T " in l}
