@@ -426,7 +426,7 @@ int gemm_coll_grouped_plan(int64_t S, int64_t K, int64_t N, int E, int act, int 
         return GC_EINVAL;
     if (S > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX || !fits(K, N) || !fits(S, N))
         return GC_ENOTSUP;
-    *plan = {};
+    *plan = {0, 1, 0};
     if (S == 0 || N == 0)
         return GC_OK;
     const GroupedPlan pl = plan_grouped(S, K, N, act == GC_ACT_SILU_GLU ? N / 2 : N, E, act == GC_ACT_SILU_GLU,

@@ -1,6 +1,7 @@
 """Host-side checks of include/gemm_coll_grouped.h (no GPU needed): every
 declared function is exported, and invalid arguments are refused before any
 HIP call; the binding refuses wrong tensors."""
+import ctypes
 import os
 import re
 import subprocess
@@ -156,3 +157,35 @@ def test_binding_refuses_wrong_tensors():
         gc.moe_combine(X, off, torch.zeros(3))
     with pytest.raises(ValueError, match="down"):
         gc.lora_add(X, X, W[0], W, torch.zeros(2), off, off)
+
+
+def test_grouped_plan():
+    """The way products are run changes with the sizes as measured: few rows stream, many groups
+    and tall ones take tiles, few tall groups tiles split along K (never without workspace)."""
+    plan = gc.grouped_plan
+    assert plan(8, 7168, 1792, 64, act="silu_glu") == dict(tiles=0, splits=1, block_rows=16)
+    assert plan(64, 7168, 1792, 8)["block_rows"] == 16
+    assert plan(128, 7168, 1792, 8)["block_rows"] == 32
+    assert plan(512, 7168, 1792, 8)["block_rows"] == 64
+    assert plan(512, 7168, 1792, 64, act="silu_glu") == dict(tiles=1, splits=1, block_rows=0)
+    few = plan(2048, 7168, 1792, 8)
+    assert few["tiles"] == 1 and few["splits"] > 1
+    assert plan(2048, 7168, 1792, 8, workspace=False)["splits"] == 1
+    assert plan(32768, 7168, 1792, 64, act="silu_glu")["splits"] == 1
+    assert plan(0, 64, 64, 4) == dict(tiles=0, splits=1, block_rows=0)
+    for bad in (dict(S=-1), dict(K=4), dict(N=12), dict(E=0), dict(E=1025), dict(cus=0)):
+        with pytest.raises(RuntimeError):
+            plan(**{**dict(S=8, K=64, N=64, E=4), **bad})
+
+
+def test_plan_struct_layout(tmp_path):
+    from tensor_bf16_gemm_amd.grouped import GroupedPlan
+    names = [n for n, _ in GroupedPlan._fields_]
+    src = tmp_path / "plan.c"
+    src.write_text('#include <stddef.h>\n#include <stdio.h>\n#include "gemm_coll_grouped.h"\nint main(void){'
+                   + "".join(f'printf("%zu ", offsetof(gc_grouped_plan,{n}));' for n in names)
+                   + 'printf("%zu\\n", sizeof(gc_grouped_plan)); return 0;}\n')
+    exe = tmp_path / "plan"
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()]
+    assert got == [getattr(GroupedPlan, n).offset for n in names] + [ctypes.sizeof(GroupedPlan)]

@@ -161,6 +161,57 @@ def test_grouped_gemm_integers(rows_per):
         assert torch.equal(got.cpu(), want.bfloat16())
 
 
+RAGGED = [600, 0, 1, 31, 32, 33, 64, 65, 97, 128, 129, 161, 193, 225, 255, 256, 257, 300, 5, 0, 513, 40, 70, 2, 90, 7,
+          100, 0, 130, 17]
+
+
+@pytest.mark.parametrize("sizes,K,N,act,kind", [
+    ([1, 0, 5, 16, 2, 0, 9, 17], 1064, 520, None, "stream 16"),
+    ([1, 0, 5, 16, 2, 0, 9, 17], 1064, 528, "silu_glu", "stream 16"),
+    ([12, 33, 0, 16], 2072, 272, "silu_glu", "stream 32"),
+    ([40, 65, 130, 7], 2072, 264, None, "stream 64"),
+    (RAGGED, 1064, 2080, None, "tiles"),
+    (RAGGED, 1064, 2080, "silu_glu", "tiles"),
+    ([2] * 29 + [60], 2056, 2072, None, "tiles"),
+    ([130, 0, 270], 4104, 4112, "silu_glu", "split"),
+    ([130, 0, 270], 4104, 4112, None, "split"),
+    ([700, 500], 7176, 2328, None, "split")])
+def test_grouped_gemm_by_plan(sizes, K, N, act, kind):
+    """Every way the products are run, over groups of very different sizes."""
+    S, E = sum(sizes), len(sizes)
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    pl = gc.grouped_plan(S, K, N, E, act=act, cus=cus)
+    got = "split" if pl["splits"] > 1 else "tiles" if pl["tiles"] else f"stream {pl['block_rows']}"
+    assert got == kind
+    g = gen(S + K)
+    T = S // 2 + 1
+    X, W = randn(g, T, K), randn(g, E, K, N, scale=K ** -0.5)
+    rows, off = torch.randint(0, T, (S,), generator=g, dtype=torch.int32), offsets_of(sizes)
+    want, tol = ref.grouped(X, W, off, rows, act)
+    d = dev(X, W, off, rows)
+    for ws in (None, False):
+        out = filled(S + 3, want.shape[1])          # (not a row past the last is touched)
+        log(f"{kind}: S={S} E={E} K={K} N={N} act={act} ws={ws} {pl}")
+        gc.grouped_gemm(*d, act=act, workspace=ws, out=out[:S])
+        ref.check(out[:S], want, tol, f"ws={ws}")
+        assert torch.all(out[S:].view(torch.int16) == SENTINEL)
+        again = gc.grouped_gemm(*d, act=act, workspace=ws)
+        assert torch.equal(again, out[:S])
+
+
+def test_grouped_gemm_many_groups():
+    """1024 groups, most of them empty or of one row."""
+    g = gen(77)
+    E, K, N = 1024, 40, 72
+    sizes = torch.randint(0, 4, (E,), generator=g)
+    sizes[::3] = 0
+    sizes[5], sizes[1023] = 300, 41
+    S = int(sizes.sum())
+    X, W, off = randn(g, S, K), randn(g, E, K, N), offsets_of(sizes.tolist())
+    want, tol = ref.grouped(X, W, off)
+    ref.check(gc.grouped_gemm(*dev(X, W, off)), want, tol, "1024 groups")
+
+
 def test_grouped_gemm_untouched_and_out_of_range():
     """Positions of no group stay as they are; rows outside X read as zeros; offsets outside
     [0, S] are clamped."""
@@ -169,7 +220,8 @@ def test_grouped_gemm_untouched_and_out_of_range():
     X, W = randn(g, T, K), randn(g, 4, K, N)
     rows = torch.randint(0, T, (S,), generator=g, dtype=torch.int32)
     rows[7], rows[8], rows[9] = -1, T, 2 ** 31 - 1
-    for off in ([3, 10, 10, 30, 41], [0, 60, 60, 90, 1000], [-5, 4, 4, 4, 4], [0, 0, 0, 0, 0]):
+    for off in ([3, 10, 10, 30, 41], [0, 60, 60, 90, 1000], [-5, 4, 4, 4, 4], [0, 0, 0, 0, 0],
+                [50, 50, 50, 50, 50]):
         off = torch.tensor(off, dtype=torch.int32)
         want, tol = ref.grouped(X, W, off, rows)
         out = filled(S, N)
