@@ -123,6 +123,17 @@ PyObject *give(PyObject *o, Tensor t)
     return THPVariable_Wrap(std::move(t));
 }
 
+// A tensor of its own over part of another's memory, which it keeps alive
+// (through the dispatcher a view costs as much as an allocation).
+Tensor part(const Tensor &buf, at::ScalarType type, int64_t byte, at::IntArrayRef shape)
+{
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                        c10::scalarTypeToTypeMeta(type));
+    t.unsafeGetTensorImpl()->set_storage_offset(byte / 4);
+    t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+    return t;
+}
+
 template <class F>
 PyObject *guarded(PyObject *const *a, Py_ssize_t n, Py_ssize_t want, F &&f)
 {
@@ -162,10 +173,12 @@ PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         const double scale = PyFloat_AsDouble(a[5]);
         if (scale == -1.0 && PyErr_Occurred())
             throw Refused{};
-        const auto i32 = x.options().dtype(at::kInt);
-        Tensor ids = at::empty({T, k}, i32), slots = at::empty({T, k}, i32);
-        Tensor weights = at::empty({T, k}, x.options().dtype(at::kFloat));
-        Tensor offsets = at::empty({E + 1}, i32), rows = at::empty({T * k}, i32);
+        // one allocation for the five outputs, each on a 256-byte boundary
+        const int64_t pairs = (T * k * 4 + 255) / 256 * 256;
+        const Tensor buf = at::empty({pairs + E / 64 * 64 + 64}, x.options().dtype(at::kInt));
+        Tensor ids = part(buf, at::kInt, 0, {T, k}), weights = part(buf, at::kFloat, pairs, {T, k});
+        Tensor rows = part(buf, at::kInt, 2 * pairs, {T * k}), slots = part(buf, at::kInt, 3 * pairs, {T, k});
+        Tensor offsets = part(buf, at::kInt, 4 * pairs, {E + 1});
         done(gemm_coll_moe_route(x.const_data_ptr(), type == at::kBFloat16 ? GC_BF16 : GC_F32,
                                  T > 1 ? x.stride(0) : E, T, (int)E, k, small(a[2], "score"), bias,
                                  PyObject_IsTrue(a[4]), (float)scale, ids.data_ptr<int32_t>(),

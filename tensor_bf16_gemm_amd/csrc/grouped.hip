@@ -106,8 +106,10 @@ int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, ui
             launch_route<false, true>(a, 1, st);
         return launched();
     }
-    // Blocks of consecutive tokens: about 512 items each, at most RT_BLOCKS.
-    const int64_t per = std::max<int64_t>({1, 512 / a.k, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS});
+    // Blocks of consecutive tokens: about 512 items each, at most RT_BLOCKS
+    // (more only where a block would pass RT_ITEMS).
+    const int64_t per = std::min<int64_t>(
+        gc::RT_ITEMS / a.k, std::max<int64_t>({1, 512 / a.k, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS}));
     const int blocks = (int)((a.T + per - 1) / per);
     a.block_tokens = (int)per;
     a.cstride = (a.E + 7) / 8 * 8;
@@ -264,11 +266,12 @@ void launch_expand(gc::ExpandArgs &a, int cus, hipStream_t st)
         }
         return;
     }
-    // Spans of columns: at most as many workgroups as have a place at once.
+    // Spans of columns: about as many workgroups as have a place at once.  (The
+    // row tiles counted here are more than there will be.)
     const int64_t places = (int64_t)cus * gc::expand_resident(steps);
     const int64_t tiles_n = (a.N + gc::EX_COLS - 1) / gc::EX_COLS;
     const int64_t tiles_m = std::min<int64_t>(a.M, (a.M + 15) / 16 + a.E);
-    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, places / tiles_m));
+    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, places * 5 / 4 / tiles_m));
     a.span = (int)((tiles_n + want - 1) / want);
     a.spans = (int)((tiles_n + a.span - 1) / a.span);
     const dim3 g((unsigned)std::min<int64_t>(tiles_m * a.spans, (int64_t)cus * 8));

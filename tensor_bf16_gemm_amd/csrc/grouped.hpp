@@ -101,18 +101,28 @@ __device__ __forceinline__ int scan_counts(int n, F &&count, int *first, int *ws
 }
 
 // first[e] = tiles of the groups before e, for tiles of `bm` positions and
-// tiles_n columns tiles; returns the number of tiles.  groups: E, or E + 1
-// with the positions past the last.
+// tiles_n columns tiles, and starts[e] = the clamped offsets; returns the
+// number of tiles.  groups: E, or E + 1 with the positions past the last.
 template <int NTH>
 __device__ __forceinline__ int scan_tiles(const int32_t *offsets, int E, int S, int groups, int bm,
-                                          int tiles_n, int *first, int *wsum)
+                                          int tiles_n, int *first, int *starts, int *wsum)
 {
     auto count = [&](int e) {
         int lo, hi;
         group_range(offsets, E, S, e, lo, hi);
+        starts[e] = lo;
         return (hi - lo + bm - 1) / bm * tiles_n;
     };
+    if (threadIdx.x == 0)
+        starts[groups] = groups == E ? min(max(offsets[E], 0), S) : S;
     return scan_counts<NTH>(groups, count, first, wsum);
+}
+
+// group_range from the starts that scan_tiles has left in LDS.
+__device__ __forceinline__ void group_bounds(const int *starts, int e, int &lo, int &hi)
+{
+    lo = __builtin_amdgcn_readfirstlane(starts[e]);
+    hi = max(__builtin_amdgcn_readfirstlane(starts[e + 1]), lo);
 }
 
 // Group of tile t: the last e with first[e] <= t (two looks of a whole wave).
@@ -176,7 +186,7 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
     static_assert((D - 1) * LOADS < 64, "vmcnt");
     static_assert(EPI != EPI_GLU || NB >= 4, "gate and up columns in one tile");
     __shared__ __attribute__((aligned(1024))) uint8_t ring[RING > SUMS ? RING : SUMS];
-    __shared__ int first[GR_GROUPS + 1];
+    __shared__ int first[GR_GROUPS + 1], starts[GR_GROUPS + 1];
     __shared__ int wsum[ST_WAVES];
     __shared__ int s_last;
 
@@ -188,7 +198,7 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
     const uint32_t N2 = (uint32_t)p.N * 2u;
     const int KT = (p.K + BK - 1) / BK;
 
-    const int tiles = scan_tiles<ST_THREADS>(p.offsets, p.E, p.S, p.E, BM, p.tiles_n, first, wsum);
+    const int tiles = scan_tiles<ST_THREADS>(p.offsets, p.E, p.S, p.E, BM, p.tiles_n, first, starts, wsum);
     if (tiles <= 0)
         return;
     Line line;
@@ -251,9 +261,7 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
         }
         const int e = __builtin_amdgcn_readfirstlane(find_group(first, p.E, t, lane));
         int lo, hi;
-        group_range(p.offsets, p.E, p.S, e, lo, hi);
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        hi = __builtin_amdgcn_readfirstlane(hi);
+        group_bounds(starts, e, lo, hi);
         const int in = t - __builtin_amdgcn_readfirstlane(first[e]);
         const int tiles_m = max((hi - lo + BM - 1) / BM, 1);
         const int nt = in / tiles_m;

@@ -85,7 +85,7 @@ __device__ __forceinline__ void load_h(const ExpandArgs &p, bool on, int m, int 
 }
 
 // Workgroups that a CU holds at once (their blocks of up fill its LDS).
-constexpr int expand_resident(int steps) { return steps <= 2 ? 3 : steps == 3 ? 2 : 1; }
+constexpr int expand_resident(int steps) { return steps == 1 ? 3 : steps <= 3 ? 2 : 1; }
 
 // KS: steps of 32 that cover r.
 template <int KS>
@@ -97,14 +97,14 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
     constexpr int PITCH = 64 * 4 + 16;                   // bytes of a row in the exchange
     __shared__ __attribute__((aligned(1024))) uint8_t ups[UP];
     __shared__ __attribute__((aligned(16))) uint8_t exchange[EX_WAVES * 16 * PITCH];
-    __shared__ int first[GR_GROUPS + 1];
+    __shared__ int first[GR_GROUPS + 1], starts[GR_GROUPS + 1];
     __shared__ int wsum[EX_THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fi = lane & 15, fg = lane >> 4;
     const int groups = p.E + (p.copy ? 1 : 0);
     const int units =
-        scan_tiles<EX_THREADS>(p.offsets, p.E, p.M, groups, BM, p.spans, first, wsum);
+        scan_tiles<EX_THREADS>(p.offsets, p.E, p.M, groups, BM, p.spans, first, starts, wsum);
     const uint32_t N2 = (uint32_t)p.N * 2u;
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base, (uint32_t)p.M * N2);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.M * N2);
@@ -118,9 +118,7 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
     for (int t = blockIdx.x; t < units; t += gridDim.x) {
         const int e = __builtin_amdgcn_readfirstlane(find_group(first, groups, t, lane));
         int lo, hi;
-        group_range(p.offsets, p.E, p.M, e, lo, hi);
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        hi = __builtin_amdgcn_readfirstlane(hi);
+        group_bounds(starts, e, lo, hi);
         const int in = t - __builtin_amdgcn_readfirstlane(first[e]);
         const int mt = in / p.spans;
         const int n_begin = (in - mt * p.spans) * p.span * EX_COLS;
@@ -226,14 +224,14 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
     __shared__ __attribute__((aligned(1024))) uint8_t own[EX_WAVES * MINE];
     __shared__ __attribute__((aligned(16))) uint8_t h_hi[XR_ROWS * H_PITCH], h_lo[XR_ROWS * H_PITCH];
     __shared__ uint32_t s_row[XR_ROWS + 16];             // byte offset of each row in base and out
-    __shared__ int first[GR_GROUPS + 1];
+    __shared__ int first[GR_GROUPS + 1], starts[GR_GROUPS + 1];
     __shared__ int wsum[EX_THREADS / 64];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fi = lane & 15, fg = lane >> 4;
     const int groups = p.E + (p.copy ? 1 : 0);
     const int units =
-        scan_tiles<EX_THREADS>(p.offsets, p.E, p.M, groups, p.span, p.spans, first, wsum);
+        scan_tiles<EX_THREADS>(p.offsets, p.E, p.M, groups, p.span, p.spans, first, starts, wsum);
     const uint32_t N2 = (uint32_t)p.N * 2u;
     const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.base, (uint32_t)p.M * N2);
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(p.out, (uint32_t)p.M * N2);
@@ -247,9 +245,7 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
     for (int t = blockIdx.x; t < units; t += gridDim.x) {
         const int e = __builtin_amdgcn_readfirstlane(find_group(first, groups, t, lane));
         int lo, hi;
-        group_range(p.offsets, p.E, p.M, e, lo, hi);
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        hi = __builtin_amdgcn_readfirstlane(hi);
+        group_bounds(starts, e, lo, hi);
         const int in = t - __builtin_amdgcn_readfirstlane(first[e]);
         const int mt = in / p.spans;
         const int n0 = (in - mt * p.spans) * XR_COLS + 128 * wave;

@@ -19,9 +19,9 @@
 //
 // Grouping: a stable counting sort by blocks of consecutive items.  Counts
 // per block first (LDS integer atomics: order does not matter to a sum), then
-// every block adds up the counts of the blocks before it by itself -- at
-// most 256 rows of 2-byte counts, read from the L2 -- which costs
-// less than a scan launch between the two kernels would.  Inside a block,
+// every block adds up the counts of the blocks before it by itself -- 256
+// rows of 2-byte counts, read from the L2 -- which costs less than a scan
+// launch between the two kernels would.  Inside a block,
 // the items of a wave that share a group find one another with one ballot per
 // bit of the group number.  Up to ROUTE_ONE_ITEMS items take one workgroup and
 // one launch for everything.
@@ -35,7 +35,9 @@ namespace gc {
 
 constexpr int RT_THREADS = 1024, RT_WAVES = RT_THREADS / 64;
 constexpr int RT_GROUPS = 1024;          // groups (experts, adapters) at most
-constexpr int RT_BLOCKS = 256;           // blocks of a many-block grouping at most
+constexpr int RT_BLOCKS = 256;           // blocks of a many-block grouping, unless
+constexpr int RT_ITEMS = 8191;           // a block's items were more than this (8 counts add up in 16 bits)
+typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
 constexpr int RT_TOP = 16;               // k at most
 // Items that one workgroup routes and groups in a single launch.
 constexpr int ROUTE_ONE_ITEMS = 1024;
@@ -578,15 +580,22 @@ __global__ __launch_bounds__(RT_THREADS) void place_kernel(RouteArgs p)
                 const int r = q + d * per_pass;
                 v[d] = *(const u32x4_t *)(p.counts + (int64_t)min(r, blocks - 1) * p.cstride + 8 * c);
             }
+            // two counts a word: AHEAD of them stay below 2^16
+            u16x2_t pre2[4] = {}, tot2[4] = {};
 #pragma unroll
             for (int d = 0; d < AHEAD; ++d) {
                 const int r = q + d * per_pass;
+                const uint32_t in = r < blocks ? ~0u : 0u, early = r < b ? ~0u : 0u;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int n = (int)((v[d][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                    tot[i] += r < blocks ? n : 0;
-                    pre[i] += r < b ? n : 0;
+                for (int i = 0; i < 4; ++i) {
+                    tot2[i] += __builtin_bit_cast(u16x2_t, v[d][i] & in);
+                    pre2[i] += __builtin_bit_cast(u16x2_t, v[d][i] & early);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                tot[i] += tot2[i >> 1][i & 1];
+                pre[i] += pre2[i >> 1][i & 1];
             }
         }
 #pragma unroll

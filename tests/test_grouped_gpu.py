@@ -124,6 +124,20 @@ def test_group_rows(T, k, groups):
         assert torch.equal(got.cpu(), want), name
 
 
+@pytest.mark.parametrize("T,k,groups", [(2_200_000, 1, 3), (140_000, 16, 1000)])
+def test_group_rows_large(T, k, groups):
+    """So many items that the blocks grow in number, nearly all of them in one group."""
+    ids = torch.randint(0, groups, (T, k), generator=gen(9), dtype=torch.int32)
+    ids[torch.rand((T, k), generator=gen(10)) < 0.9] = 1
+    key, order = torch.sort(ids.flatten(), stable=True)
+    g = gc.group_rows(ids.to(DEV), groups)
+    assert torch.equal(g.offsets.cpu(), torch.searchsorted(key, torch.arange(groups + 1, dtype=torch.int32)).int())
+    assert torch.equal(g.rows.cpu(), (order // k).int())
+    slots = torch.empty_like(order)
+    slots[order] = torch.arange(T * k)
+    assert torch.equal(g.slots.cpu().flatten().long(), slots)
+
+
 # ---- grouped products ----
 
 SIZES = [[1], [0, 0, 5, 0], [16, 17, 0, 33, 1], [64, 65, 1, 63], [130, 0, 257], [7] * 30, [300, 520, 3],
