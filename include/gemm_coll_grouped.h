@@ -23,7 +23,8 @@
  * no device memory allocated; a negative return launches nothing.  Outputs
  * must not overlap inputs (lora_add's out may be its base).  A buffer
  * addressed as one (X, out, one expert's weights) must be below 2 GiB
- * (GC_ENOTSUP); the weights of all experts together may be larger.
+ * (GC_ENOTSUP; so are weights of more than 2^24 columns); the weights of all
+ * experts together may be larger.
  *
  * Groups.  A grouping of n items into `groups` groups is
  *   offsets  int32 [groups + 1]: group g owns positions [offsets[g], offsets[g+1])

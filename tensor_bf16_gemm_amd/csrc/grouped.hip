@@ -47,6 +47,10 @@ bool good4(const void *p) { return p && aligned(p, 4); }
 // sentinel at 2^31.
 bool fits(int64_t rows, int64_t cols) { return cols == 0 || rows < ((int64_t)1 << 30) / cols; }
 
+// Rows of weights past K are addressed too, and must read as zeros: up to 31
+// rows past the buffer (127 for the adapters' up) the offset stays in 32 bits.
+constexpr int64_t kMaxCols = (int64_t)1 << 24;
+
 // Workspace: counters (4 KiB, zero between launches), then room for one of
 // the partial tiles of the streaming kernel (two of at most kPartBytes per
 // workgroup), the fp32 sums of products split along K, the counts of a
@@ -376,7 +380,7 @@ int gemm_coll_grouped_gemm(const gc_bf16 *X, int64_t T, const gc_bf16 *W, const 
         return GC_EINVAL;
     if (K % 8 != 0 || N % (act == GC_ACT_SILU_GLU ? 16 : 8) != 0 || (!rows && T < S))
         return GC_EINVAL;
-    if (T > INT32_MAX || S > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX)
+    if (T > INT32_MAX || S > INT32_MAX / 2 || K > INT32_MAX || N > kMaxCols)
         return GC_ENOTSUP;
     if (!fits(T, K) || !fits(K, N) || !fits(S, N))
         return GC_ENOTSUP;
@@ -427,7 +431,7 @@ int gemm_coll_grouped_plan(int64_t S, int64_t K, int64_t N, int E, int act, int 
         (act != GC_ACT_NONE && act != GC_ACT_SILU_GLU) || K % 8 != 0 ||
         N % (act == GC_ACT_SILU_GLU ? 16 : 8) != 0)
         return GC_EINVAL;
-    if (S > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX || !fits(K, N) || !fits(S, N))
+    if (S > INT32_MAX / 2 || K > INT32_MAX || N > kMaxCols || !fits(K, N) || !fits(S, N))
         return GC_ENOTSUP;
     *plan = {0, 1, 0};
     if (S == 0 || N == 0)
@@ -485,7 +489,7 @@ int gemm_coll_lora_add(const gc_bf16 *base, const gc_bf16 *X, const gc_bf16 *dow
         return GC_EINVAL;
     if (K % 8 != 0 || N % 8 != 0 || r % 8 != 0)
         return GC_EINVAL;
-    if (M > INT32_MAX / 2 || K > INT32_MAX || N > INT32_MAX)
+    if (M > INT32_MAX / 2 || K > INT32_MAX || N > kMaxCols)
         return GC_ENOTSUP;
     if (!fits(M, K) || !fits(M, N) || !fits(M, r) || !fits(K, r) || !fits(r, N))
         return GC_ENOTSUP;

@@ -92,7 +92,7 @@ def test_grouped_gemm_refuses(L, kw):
 
 
 @pytest.mark.parametrize("kw", [dict(T=1 << 24), dict(S=1 << 24), dict(K=1 << 15, N=1 << 15),
-                                dict(T=1 << 32), dict(K=1 << 40)])
+                                dict(T=1 << 32), dict(K=1 << 40), dict(K=8, N=(1 << 24) + 8)])
 def test_grouped_gemm_too_large(L, kw):
     assert gemm(L, **{**dict(S=100, rows=P), **kw}) == gc.GC_ENOTSUP
 
