@@ -100,8 +100,10 @@ void launch_route(const gc::RouteArgs &a, int blocks, hipStream_t st)
 int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, uint64_t bytes,
                     hipStream_t st)
 {
+    // One workgroup for everything: up to two tokens for each row of lanes.
     const int64_t items = (int64_t)a.T * a.k;
-    if (items <= gc::ROUTE_ONE_ITEMS) {
+    const int at_once = gc::RT_THREADS / route_lanes(a.E);
+    if (items <= gc::ROUTE_ONE_ITEMS && (!route || a.T <= 2 * at_once)) {
         if (!route)
             hipLaunchKernelGGL((gc::route_kernel<16, 0, false, true>), dim3(1), dim3(gc::RT_THREADS), 0, st, a);
         else if (bf16)
@@ -110,10 +112,12 @@ int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, ui
             launch_route<false, true>(a, 1, st);
         return launched();
     }
-    // Blocks of consecutive tokens: about 512 items each, at most RT_BLOCKS
-    // (more only where a block would pass RT_ITEMS).
+    // Blocks of consecutive tokens: as many as a workgroup routes at a time, or
+    // about 512 items to group; at most RT_BLOCKS (more only where a block
+    // would pass RT_ITEMS).
+    const int64_t few = route ? std::min(at_once, std::max(1, 512 / a.k)) : std::max(1, 512 / a.k);
     const int64_t per = std::min<int64_t>(
-        gc::RT_ITEMS / a.k, std::max<int64_t>({1, 512 / a.k, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS}));
+        gc::RT_ITEMS / a.k, std::max<int64_t>(few, (a.T + gc::RT_BLOCKS - 1) / gc::RT_BLOCKS));
     const int blocks = (int)((a.T + per - 1) / per);
     a.block_tokens = (int)per;
     a.cstride = (a.E + 7) / 8 * 8;
@@ -194,14 +198,15 @@ struct GroupedPlan {
 // The cheapest by three estimates in us, fitted to measurements at K = 512 to
 // 7168, N = 512 to 7168, 4 to 64 groups of 1 to 1024 rows:
 //   stream   every ceil(rows / tile rows) pass reads the weights at 5.3 TB/s,
-//            and 8 us
-//   tiles    rounds of tiles (one at least) of 0.6 us a K-step, 0.93 with 256
-//            rows; the weights at 6.3 TB/s at best; and 12 us
+//            twice as much (half for PLAIN) where its row pieces are not whole
+//            lines of 128 bytes; and 8 us
+//   tiles    rounds of tiles (one at least) of 0.6 us a K-step, 0.93
+//            with 256 rows; the weights at 6.3 TB/s at best; and 12 us
 //   split    the pieces' rounds the same but 15 % slower, 22 us, and the sums
 //            written and read at 4 TB/s; where the sums have room
 // (us measured, stream / tiles / split: K 7168, N 1792, 64 groups of 16 rows
-// 282 / 272 / -; 8 groups of 8 rows 38 / 163 / 57, of 64 rows 48 / 175 / 77,
-// of 192 rows 122 / 213 / 123, of 256 rows 163 / 225 / 140.)  Groups are taken
+// 282 / 272 / -; 8 groups of 8 rows 37 / 163 / 57, of 64 rows 43 / 175 / 77,
+// of 192 rows 122 / 213 / 80, of 256 rows 163 / 225 / 100.)  Groups are taken
 // as equally large, as many as there are rows at most; a stream tile has room
 // for twice the average rows, for real groups are not equal.
 GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool glu, bool workspace, int cus)
@@ -211,14 +216,16 @@ GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool
     const int kt = (int)((K + gc::BK - 1) / gc::BK);
     const double w = (double)used * K * N * 2e-6;                       // MB of weights
     pl.blocks = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-    const double t_stream = (double)((rows + 16 * pl.blocks - 1) / (16 * pl.blocks)) * w / 5.3 + 8;
+    const double lines = (N % 64 != 0 || F % 64 != 0) ? (glu ? 2.0 : 1.5) : 1.0;
+    const double t_stream = (double)((rows + 16 * pl.blocks - 1) / (16 * pl.blocks)) * w * lines / 5.3 + 8;
     const int64_t bn = glu ? gc::BN / 2 : gc::BN, tiles_n = (F + bn - 1) / bn;
     const double tiles = (double)used * std::max(1.0, (double)rows / 256 + 0.5) * tiles_n;
     const double step = 0.6 + 0.0013 * std::min<int64_t>(rows, 256);
+    auto rounds = [&](double units) { return std::max(1.0, units / cus); };
     pl.splits = 1;
-    double best = 12 + std::max(std::max(1.0, tiles / cus) * kt * step, w / 6.3);
+    double best = 12 + std::max(rounds(tiles) * kt * step, w / 6.3);
     for (int q = 2; workspace && q <= 8 && kt / q >= 16 && q * S * N * 4 <= kSumBytes; ++q) {
-        const double t = 22 + std::max(1.15 * std::max(1.0, q * tiles / cus) * ((kt + q - 1) / q) * step, w / 6.3) +
+        const double t = 22 + std::max(1.15 * rounds(q * tiles) * ((kt + q - 1) / q) * step, w / 6.3) +
                          (double)q * S * N * 8e-6 / 4.0;
         if (t < best) {
             best = t;

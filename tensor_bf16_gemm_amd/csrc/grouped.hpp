@@ -399,19 +399,33 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
                 continue;
             }
         }
-        // sum of block b over the pieces of a cut tile, in the order of K
-        auto final_sum = [&](int b) {
-            if (!cut)
-                return block_sum(b);
-            f32x4_t x = {0.f, 0.f, 0.f, 0.f};
+        // Sums of n blocks (numbers at[]): of a cut tile over its pieces, in the
+        // order of K, every piece's blocks asked for together.
+        auto final_sums = [&](auto &x, const auto &at, auto count) {
+            constexpr int n = decltype(count)::value;
+            if (!cut) {
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+                    x[i] = block_sum(at[i]);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < n; ++i)
+                x[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
             for (int w = w_first; w <= w_last; ++w) {
                 const uint32_t slot = (uint32_t)(2 * w + (w == w_first ? 1 : 0));
-                x += __builtin_bit_cast(
-                    f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                 rp, (int)(slot * (uint32_t)(RB * NB * 1024) + (uint32_t)(b * 1024 + lane * 16)),
-                                 0, CPOL_SYS));
+                f32x4_t y[n];
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+                    y[i] = __builtin_bit_cast(
+                        f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                     rp, (int)(slot * (uint32_t)(RB * NB * 1024) + (uint32_t)(at[i] * 1024 + lane * 16)),
+                                     0, CPOL_SYS));
+#pragma unroll
+                for (int i = 0; i < n; ++i)
+                    x[i] += y[i];
             }
-            return x;
         };
 
         // ---- epilogue ----
@@ -425,18 +439,34 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
                     *(f32x4_t *)(p.sums + ((size_t)piece * p.S + m) * p.N + n) = x;
             }
         } else {
-            constexpr int PAIRS = EPI == EPI_GLU ? NB / 4 : NB / 2;
-            for (int u = wave; u < RB * PAIRS; u += ST_WAVES) {
+            // A unit is a pair of neighbouring blocks (for GLU, gate and up); a
+            // wave takes every fourth.
+            constexpr int PAIRS = EPI == EPI_GLU ? NB / 4 : NB / 2, PER = EPI == EPI_GLU ? 4 : 2;
+            constexpr int UNITS = (RB * PAIRS + ST_WAVES - 1) / ST_WAVES;
+            f32x4_t x[UNITS * PER];
+            int at[UNITS * PER];
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                const int u = min(wave + ST_WAVES * k, RB * PAIRS - 1);
                 const int i = u / PAIRS, j = 2 * (u - i * PAIRS);
-                f32x4_t x = final_sum(i * NB + j), y = final_sum(i * NB + j + 1);
-                if (EPI == EPI_GLU) {
-                    x = silu_mul(x, final_sum(i * NB + j + NB / 2));
-                    y = silu_mul(y, final_sum(i * NB + j + 1 + NB / 2));
+#pragma unroll
+                for (int d = 0; d < PER; ++d)
+                    at[PER * k + d] = i * NB + j + (d & 1) + (d >> 1) * (NB / 2);
+            }
+            final_sums(x, at, std::integral_constant<int, UNITS * PER>{});
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+                const int u = wave + ST_WAVES * k;
+                const int i = u / PAIRS, j = 2 * (u - i * PAIRS);
+                f32x4_t a = x[PER * k], b = x[PER * k + 1];
+                if constexpr (EPI == EPI_GLU) {
+                    a = silu_mul(a, x[PER * k + 2]);
+                    b = silu_mul(b, x[PER * k + 3]);
                 }
-                const u32x4_t pk = pack_pair(x, y);
+                const u32x4_t pk = pack_pair(a, b);
                 const int m = m0 + 16 * i + fi;
                 const int n = nt * (EPI == EPI_GLU ? BN / 2 : BN) + 16 * j + p8;
-                if (m < hi && n < F)
+                if (u < RB * PAIRS && m < hi && n < F)
                     *(u32x4_t *)(p.out + (size_t)m * F + n) = pk;
             }
         }

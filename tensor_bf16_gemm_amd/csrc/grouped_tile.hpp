@@ -258,7 +258,10 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
     const int splits = SUMS ? p.splits : 1;
     const int KT = (p.K + BK - 1) / BK, piece_steps = (KT + splits - 1) / splits;
     const int units = tiles * splits;
-    // Queue x holds hands x, x + 8, ... of TK_HAND units.
+    // Queue x holds hands x, x + 8, ... of TK_HAND units (an eighth of the units
+    // where they are few: 8 groups of 512 rows, K 7168, N 1792 on two queues
+    // took 305 us, on eight 122).
+    const int hand = max(min(TK_HAND, (units + TK_QUEUES - 1) / TK_QUEUES), 1);
     int x = blockIdx.x & (TK_QUEUES - 1), tried = 0, mine = blockIdx.x / TK_QUEUES;
     const int per_queue = (G + TK_QUEUES - 1) / TK_QUEUES;
     // Next unit for this workgroup, or -1 (thread 0 only).
@@ -274,7 +277,7 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
                 t = mine;
                 mine += per_queue;
             }
-            t = (t / TK_HAND * TK_QUEUES + x) * TK_HAND + t % TK_HAND;
+            t = (t / hand * TK_QUEUES + x) * hand + t % hand;
             if (t < units)
                 return t;
         }

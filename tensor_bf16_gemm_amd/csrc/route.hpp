@@ -8,7 +8,7 @@
 // that is left over gets id -1 and weight 0.
 //
 // A token is a row of 16 lanes (four tokens per wave) for up to 256 experts,
-// else a whole wave; each lane holds V consecutive experts.  A (key, index)
+// else a whole wave; each lane holds V experts.  A (key, index)
 // pair is packed into one number -- an order-preserving key, then the index
 // counted downwards -- so that one maximum compares both and no two are
 // equal: 16 + 16 bits of a word for bf16 logits, else 32 + 20 bits of the
@@ -299,7 +299,9 @@ __device__ __forceinline__ float logit(const RouteArgs &p, int t, int e)
 template <int LPT, int V, bool BF16, class Pair>
 __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, int &id, float &w)
 {
-    const int e0 = j * V;
+    // The lane's experts: V neighbours where they are whole aligned vectors,
+    // else every LPT-th (which the lanes of a token read side by side).
+    const int e0 = p.vec ? j * V : j, es = p.vec ? 1 : LPT;
     const bool soft = p.score == SCORE_SOFTMAX;
     float x[V];
     if (p.vec && e0 < p.E) {
@@ -317,12 +319,12 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, in
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            x[i] = e0 + i < p.E ? logit<BF16>(p, t, e0 + i) : -__builtin_huge_valf();
+            x[i] = e0 + i * es < p.E ? logit<BF16>(p, t, e0 + i * es) : -__builtin_huge_valf();
     }
     typename Pair::P a[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        a[i] = Pair::make(order_key(x[i]), e0 + i);
+        a[i] = Pair::make(order_key(x[i]), e0 + i * es);
     // For a softmax over all experts: its maximum and its sum.
     float high = 0.f, total = 1.f;
     if (soft && (p.bias || !p.renorm)) {
@@ -342,7 +344,7 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, in
         for (int i = 0; i < V; ++i)
             if (a[i] != Pair::none()) {
                 const float s = soft ? soft_term(x[i], high) / total : sigmoid(x[i]);
-                a[i] = Pair::make(order_key(s + p.bias[e0 + i]), e0 + i);
+                a[i] = Pair::make(order_key(s + p.bias[e0 + i * es]), e0 + i * es);
             }
     }
     sort_pairs(a);

@@ -187,6 +187,7 @@ RAGGED = [600, 0, 1, 31, 32, 33, 64, 65, 97, 128, 129, 161, 193, 225, 255, 256, 
     (RAGGED, 1064, 2080, None, "tiles"),
     (RAGGED, 1064, 2080, "silu_glu", "tiles"),
     ([2] * 29 + [60], 2056, 2072, None, "tiles"),
+    ([2] * 59 + [60], 1064, 2080, None, "tiles"),
     ([130, 0, 270], 4104, 4112, "silu_glu", "split"),
     ([130, 0, 270], 4104, 4112, None, "split"),
     ([700, 500], 7176, 2328, None, "split")])
