@@ -296,15 +296,16 @@ __device__ __forceinline__ float logit(const RouteArgs &p, int t, int e)
 // Routes one token per LPT lanes.  Lane j < k of the token returns with the
 // j-th choice's expert (-1: none) in `id` and its weight in `w`.  `t` is the
 // lane's token, which must exist.
-template <int LPT, int V, bool BF16, class Pair>
+template <int LPT, int V, bool BF16, bool VEC, class Pair>
 __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, int &id, float &w)
 {
-    // The lane's experts: V neighbours where they are whole aligned vectors,
-    // else every LPT-th (which the lanes of a token read side by side).
-    const int e0 = p.vec ? j * V : j, es = p.vec ? 1 : LPT;
+    // The lane's experts: V neighbours where they are whole aligned vectors
+    // (VEC), else every LPT-th (which the lanes of a token read side by side).
+    constexpr int es = VEC ? 1 : LPT;
+    const int e0 = VEC ? j * V : j;
     const bool soft = p.score == SCORE_SOFTMAX;
     float x[V];
-    if (p.vec && e0 < p.E) {
+    if (VEC && e0 < p.E) {
         if constexpr (BF16) {
             uint16_t b[V];
             __builtin_memcpy(b, __builtin_assume_aligned((const uint16_t *)p.logits + (int64_t)t * p.stride + e0,
@@ -350,17 +351,25 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, in
     sort_pairs(a);
     const auto none = Pair::none();
     auto mine = none, best = none;
-    for (int r = 0; r < p.k; ++r) {
-        const auto top = token_max<LPT>(a[0]);
-        if (r == 0)
-            best = top;
-        mine = Pair::pick(j == r, top, mine);
-        const bool won = a[0] == top;            // (none: its list is empty, moving it changes nothing)
+    // (a list is never asked for more than k of its pairs)
+    auto rounds = [&](auto deep) {
+        constexpr int D = decltype(deep)::value;
+        for (int r = 0; r < p.k; ++r) {
+            const auto top = token_max<LPT>(a[0]);
+            if (r == 0)
+                best = top;
+            mine = Pair::pick(j == r, top, mine);
+            const bool won = a[0] == top;        // (none: its list is empty, moving it changes nothing)
 #pragma unroll
-        for (int i = 0; i + 1 < V; ++i)
-            a[i] = Pair::pick(won, a[i + 1], a[i]);
-        a[V - 1] = Pair::pick(won, none, a[V - 1]);
-    }
+            for (int i = 0; i + 1 < D; ++i)
+                a[i] = Pair::pick(won, a[i + 1], a[i]);
+            a[D - 1] = Pair::pick(won, none, a[D - 1]);
+        }
+    };
+    if (V > 8 && p.k <= 8)
+        rounds(std::integral_constant<int, (V > 8 ? 8 : V)>{});
+    else
+        rounds(std::integral_constant<int, V>{});
     const bool chosen = mine != none;
     id = chosen ? Pair::expert(mine) : -1;
     float val = key_value(Pair::key(mine));
@@ -490,10 +499,20 @@ __global__ __launch_bounds__(RT_THREADS) void route_kernel(RouteArgs p)
                 break;                                   // no token in this wave
             int id;
             float w;
-            if (BF16 && !p.bias)
-                route_token<LPT, V, BF16, NarrowPair>(p, min(t, t1 - 1), j, id, w);
-            else
-                route_token<LPT, V, BF16, WidePair>(p, min(t, t1 - 1), j, id, w);
+            const int tl = min(t, t1 - 1);
+            if constexpr (BF16) {
+                if (p.bias)
+                    route_token<LPT, V, BF16, false, WidePair>(p, tl, j, id, w);
+                else if (p.vec)
+                    route_token<LPT, V, BF16, true, NarrowPair>(p, tl, j, id, w);
+                else
+                    route_token<LPT, V, BF16, false, NarrowPair>(p, tl, j, id, w);
+            } else {
+                if (p.vec)
+                    route_token<LPT, V, BF16, true, WidePair>(p, tl, j, id, w);
+                else
+                    route_token<LPT, V, BF16, false, WidePair>(p, tl, j, id, w);
+            }
             if (j < p.k && t < t1) {
                 const int flat = t * p.k + j;
                 p.ids[flat] = id;
