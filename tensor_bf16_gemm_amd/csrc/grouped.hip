@@ -205,10 +205,13 @@ struct GroupedPlan {
 //   split    the pieces' rounds the same but 15 % slower, 22 us, and the sums
 //            written and read at 4 TB/s; where the sums have room
 // (us measured, stream / tiles / split: K 7168, N 1792, 64 groups of 16 rows
-// 282 / 272 / -; 8 groups of 8 rows 37 / 163 / 57, of 64 rows 43 / 175 / 77,
-// of 192 rows 122 / 213 / 80, of 256 rows 163 / 225 / 100.)  Groups are taken
-// as equally large, as many as there are rows at most; a stream tile has room
-// for twice the average rows, for real groups are not equal.
+// 286 / 276 / 296; 8 groups of 8 rows 37 / 93 / 42, of 64 rows 44 / 101 / 48,
+// of 192 rows 119 / 119 / 75, of 256 rows 154 / 131 / 90.  Over 170 random
+// sizes the choice is 4.5 % slower than the best of the three on average, over
+// 221 of equal groups 2.2 %, 82 % at worst: the tiles' step is taken for a full
+// chip and too long for few tiles.)  Groups are taken as equally large, as many
+// as there are rows at most; a stream tile has room for twice the average rows,
+// for real groups are not equal.
 GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool glu, bool workspace, int cus)
 {
     GroupedPlan pl = {};

