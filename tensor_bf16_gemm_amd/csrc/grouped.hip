@@ -195,23 +195,29 @@ struct GroupedPlan {
     int blocks;      // stream_kernel: blocks of 16 rows in a tile
 };
 
-// The cheapest by three estimates in us, fitted to measurements at K = 512 to
-// 7168, N = 512 to 7168, 4 to 64 groups of 1 to 1024 rows:
-//   stream   every ceil(rows / tile rows) pass reads the weights at 5.3 TB/s,
-//            twice as much (half for PLAIN) where its row pieces are not whole
-//            lines of 128 bytes; and 8 us
-//   tiles    rounds of tiles (one at least) of 0.6 us a K-step, 0.93
-//            with 256 rows; the weights at 6.3 TB/s at best; and 12 us
-//   split    the pieces' rounds the same but 15 % slower, 22 us, and the sums
-//            written and read at 4 TB/s; where the sums have room
-// (us measured, stream / tiles / split: K 7168, N 1792, 64 groups of 16 rows
-// 286 / 276 / 296; 8 groups of 8 rows 37 / 93 / 42, of 64 rows 44 / 101 / 48,
-// of 192 rows 119 / 119 / 75, of 256 rows 154 / 131 / 90.  Over 170 random
-// sizes the choice is 4.5 % slower than the best of the three on average, over
-// 221 of equal groups 2.2 %, 82 % at worst: the tiles' step is taken for a full
-// chip and too long for few tiles.)  Groups are taken as equally large, as many
-// as there are rows at most; a stream tile has room for twice the average rows,
-// for real groups are not equal.
+// The cheapest by three estimates in us, fitted to all of them measured at 391
+// sizes (K 264 to 7168, N 264 to 7168, 1 to 64 groups of 1 to 3900 rows, equal
+// and skewed):
+//   stream   reads the weights at 6 TB/s, and again for every further tile of
+//            rows at 11, or at 21 where the L2s hold them; twice as much (half
+//            for PLAIN) where its row pieces are not whole lines of 128 bytes;
+//            each 16 rows of a tile take its CU 0.037 us a K-step, and 19
+//            K-steps more to begin and end; and 2.5 us
+//   tiles    rounds of tiles (one at least) of 0.36 us a K-step, 0.55 with 256
+//            rows, 0.72 with 256 rows on every CU, and 1.1 K-steps more; the
+//            weights at 6.2 TB/s at best; and 18 us
+//   split    in 2, 3, 4, 6 or 8 pieces: their rounds the same, 25 us, and the
+//            sums written and read at 4 TB/s; where the sums have room
+// At the sizes of the fit the choice is 1.1 % slower than the best of all on
+// average, 34 % at worst.  At 204 random sizes outside it, estimates without a
+// tile's beginning and end and with the step of a full chip took 1.6 % longer
+// on average, between 0.78 and 1.75 times as long.
+// us measured, stream / tiles / best split: K 7168, N 1792, 64 groups of 16
+// rows with GLU 286 / 276 / 296; 8 groups of 8 rows 37 / 93 / 42, of 64 rows
+// 44 / 101 / 48, of 192 rows 119 / 119 / 75, of 256 rows 154 / 131 / 90, of
+// 1024 rows 453 / 181 / -.  Groups are taken as equally large, as many as there
+// are rows at most; a stream tile has room for twice the average rows, for real
+// groups are not equal.
 GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool glu, bool workspace, int cus)
 {
     GroupedPlan pl = {};
@@ -220,15 +226,20 @@ GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool
     const double w = (double)used * K * N * 2e-6;                       // MB of weights
     pl.blocks = rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
     const double lines = (N % 64 != 0 || F % 64 != 0) ? (glu ? 2.0 : 1.5) : 1.0;
-    const double t_stream = (double)((rows + 16 * pl.blocks - 1) / (16 * pl.blocks)) * w * lines / 5.3 + 8;
+    const int64_t passes = (rows + 16 * pl.blocks - 1) / (16 * pl.blocks), strip = glu ? 64 : 128;
+    const double work = (double)used * passes * pl.blocks * ((F + strip - 1) / strip) * (kt + 19) / cus;
+    const double t_stream = 2.5 + w * lines * (1 / 6.0 + (double)(passes - 1) / (w > 32 ? 11.0 : 21.0)) + 0.037 * work;
     const int64_t bn = glu ? gc::BN / 2 : gc::BN, tiles_n = (F + bn - 1) / bn;
     const double tiles = (double)used * std::max(1.0, (double)rows / 256 + 0.5) * tiles_n;
-    const double step = 0.6 + 0.0013 * std::min<int64_t>(rows, 256);
-    auto rounds = [&](double units) { return std::max(1.0, units / cus); };
+    auto rounds = [&](double units, int steps) {
+        const double busy = std::min(1.0, units / cus), height = (double)std::min<int64_t>(rows, 256);
+        return std::max(1.0, units / cus) * (steps + 1.1) * (0.36 + 0.097 * busy + height * (0.00074 + 0.00027 * busy));
+    };
     pl.splits = 1;
-    double best = 12 + std::max(rounds(tiles) * kt * step, w / 6.3);
-    for (int q = 2; workspace && q <= 8 && kt / q >= 16 && q * S * N * 4 <= kSumBytes; ++q) {
-        const double t = 22 + std::max(1.15 * rounds(q * tiles) * ((kt + q - 1) / q) * step, w / 6.3) +
+    double best = 18 + std::max(rounds(tiles, kt), w / 6.2);
+    for (int q = 2; workspace && q <= 8 && kt / q >= 16 && q * S * N * 4 <= kSumBytes;
+         q += q < 4 ? 1 : 2) {
+        const double t = 25 + std::max(rounds(q * tiles, (kt + q - 1) / q), w / 6.2) +
                          (double)q * S * N * 8e-6 / 4.0;
         if (t < best) {
             best = t;
