@@ -139,8 +139,8 @@ int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, con
  *   out[m] = bf16( base[m] + (scale[a] * X[m] . down[a]) . up[a] )
  * with X [M][K], base and out [M][N], down [G][K][r], up [G][r][N],
  * scale float [G], offsets and rows [M] a grouping of the M rows by adapter.
- * The middle activations are fp32 sums, multiplied as two bf16 (16 bits of
- * mantissa).  Rows in no group: out is base (base == out: untouched).
+ * The middle activations are fp32 sums and are multiplied as such (all 24
+ * bits).  Rows in no group: out is base (base == out: untouched).
  * r <= 128, a multiple of 8; G <= 1023.  Needs
  * gemm_coll_lora_workspace_bytes(M, r) bytes of workspace.
  */

@@ -2,9 +2,11 @@
 // position i of the rows grouped by adapter, with m = rows[i],
 //   out[m] = bf16(base[m] + H[i] . up[a(i)]),   H[i] = scale[a] X[m] . down[a],
 // where stream_kernel has left X[m] . down[a] as fp32 sums over pieces of K.
-// H enters the matrix cores as the sum of two bf16 (the rounded value and the
-// rounded rest), which keeps 16 bits of it: with one bf16 the middle
-// rounding would be as large as that of the output.
+// H enters the matrix cores as three bf16 that take 8 leading bits each and
+// add up to all 24 of the fp32 value: nothing is rounded between the fp32
+// sums and the output.  (Two bf16 would leave an error of 2^-16 of
+// H, enough to round one output in a thousand the other way.  The third costs
+// 0.1 to 0.6 us: 56.4 -> 57.1 at M = 4096, N = 6288, r = 64.)
 //
 // Rows are read and written once and there are at most r <= 128 products per
 // output: the kernels are bound by the traffic of base and out.  In both, the
@@ -14,7 +16,7 @@
 //
 // expand_rows_kernel, many rows per group: a wave keeps r x 128 values of up
 // in registers and walks down the rows of its workgroup, whose H stands in LDS
-// as bf16; nothing but rows of base and out moves in the loop, and the next
+// as fp32; nothing but rows of base and out moves in the loop, and the next
 // rows are on their way while these are multiplied.  (With up in LDS and the
 // walk along the columns, every tile of 256 columns waited for its block of
 // up, its base and the last stores in turn: M = 4096, N = 6288, r = 64 took
@@ -55,12 +57,12 @@ __device__ __forceinline__ u32x4_t add_base(f32x4_t a, f32x4_t b, u32x4_t base)
 }
 
 // Eight neighbouring values of H for position m: the sums over the pieces of
-// K, in order, times the scale, as two bf16 whose sum carries 16 bits.
+// K, in order, times the scale.
 template <int AHEAD>
-__device__ __forceinline__ void load_h(const ExpandArgs &p, bool on, int m, int k, float scale, u32x4_t &hi,
-                                       u32x4_t &lo)
+__device__ __forceinline__ void load_h(const ExpandArgs &p, bool on, int m, int k, float scale, f32x4_t &x,
+                                       f32x4_t &y)
 {
-    f32x4_t x = {0.f, 0.f, 0.f, 0.f}, y = x;
+    x = y = (f32x4_t){0.f, 0.f, 0.f, 0.f};
     const float *at = p.sums + (on ? (size_t)m * p.r + k : 0);
     for (int c = 0; c < p.splits; c += AHEAD) {
         f32x4_t a[AHEAD], b[AHEAD];
@@ -81,10 +83,23 @@ __device__ __forceinline__ void load_h(const ExpandArgs &p, bool on, int m, int 
     }
     x *= scale;
     y *= scale;
-    const u32x2_t hx = pack_bf16x4(x), hy = pack_bf16x4(y);
-    const u32x2_t lx = pack_bf16x4(x - unpack_bf16x4(hx)), ly = pack_bf16x4(y - unpack_bf16x4(hy));
-    hi = (u32x4_t){hx[0], hx[1], hy[0], hy[1]};
-    lo = (u32x4_t){lx[0], lx[1], ly[0], ly[1]};
+}
+
+// The leading 8 bits of eight fp32 values as bf16 (cut off, so that no finite
+// value becomes infinite and the rest keeps its sign), the values left as the
+// rest.  Three times leaves nothing of 24 bits.
+__device__ __forceinline__ bf16x8_t take_bf16(f32x4_t &x, f32x4_t &y)
+{
+    u32x4_t r;
+    const u32x4_t a = __builtin_bit_cast(u32x4_t, x), b = __builtin_bit_cast(u32x4_t, y);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        r[i] = __builtin_amdgcn_perm(a[2 * i + 1], a[2 * i], 0x07060302u);
+        r[i + 2] = __builtin_amdgcn_perm(b[2 * i + 1], b[2 * i], 0x07060302u);
+    }
+    x -= __builtin_bit_cast(f32x4_t, a & 0xFFFF0000u);
+    y -= __builtin_bit_cast(f32x4_t, b & 0xFFFF0000u);
+    return __builtin_bit_cast(bf16x8_t, r);
 }
 
 // Workgroups that a CU holds at once (their blocks of up fill its LDS).
@@ -161,16 +176,17 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             old[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(i, n_begin), 0, 0);
-        // H of the rows, as two bf16 fragments
-        bf16x8_t h[KS], l[KS];
+        // H of the rows, as three bf16 fragments
+        bf16x8_t h[KS][3];
         const float sc = delta ? p.scale[e] : 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int m = m0 + fi, k = 32 * s + 8 * fg;
-            u32x4_t a, b;
-            load_h<KS == 1 ? 8 : 4>(p, delta && m < hi && k < p.r, m, k, sc, a, b);
-            h[s] = __builtin_bit_cast(bf16x8_t, a);
-            l[s] = __builtin_bit_cast(bf16x8_t, b);
+            f32x4_t x, y;
+            load_h<KS == 1 ? 8 : 4>(p, delta && m < hi && k < p.r, m, k, sc, x, y);
+#pragma unroll
+            for (int d = 0; d < 3; ++d)
+                h[s][d] = take_bf16(x, y);
         }
         for (int n0 = n_begin; n0 < n_end; n0 += EX_COLS) {
             wait_vmcnt<0>();                     // this wave's part of the block of up has landed,
@@ -191,8 +207,9 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
                     bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
                         (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a + 4 * 512));
                     const bf16x8_t fa = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s], acc[j], 0, 0, 0);
-                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, l[s], acc[j], 0, 0, 0);
+#pragma unroll
+                    for (int d = 0; d < 3; ++d)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s][d], acc[j], 0, 0, 0);
                 }
             // (LDS operations of a wave are done in order: no wait between them)
 #pragma unroll
@@ -220,12 +237,12 @@ template <int KS>
 __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kernel(ExpandArgs p)
 {
     constexpr int NB = 8;                                // 16-column blocks of a wave
-    constexpr int H_PITCH = 64 * KS + 16;                // bytes of a row of H in LDS
+    constexpr int H_PITCH = 128 * KS + 16;               // bytes of a row of H in LDS
     constexpr int PITCH = 128 * 4 + 16;                  // bytes of a row in the exchange
     constexpr int MINE = 16 * PITCH;                     // bytes of a wave: a block of up, later the exchange
     static_assert(MINE >= 32 * 256, "a block of up");
     __shared__ __attribute__((aligned(1024))) uint8_t own[EX_WAVES * MINE];
-    __shared__ __attribute__((aligned(16))) uint8_t h_hi[XR_ROWS * H_PITCH], h_lo[XR_ROWS * H_PITCH];
+    __shared__ __attribute__((aligned(16))) uint8_t hs[XR_ROWS * H_PITCH];
     __shared__ uint32_t s_row[XR_ROWS + 16];             // byte offset of each row in base and out
     __shared__ int first[GR_GROUPS + 1], starts[GR_GROUPS + 1];
     __shared__ int wsum[EX_THREADS / 64];
@@ -277,10 +294,10 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
             const float sc = p.scale[e];
             for (int i = tid; i < (count + 15) / 16 * 16 * 4 * KS; i += EX_THREADS) {
                 const int r = i / (4 * KS), k = 8 * (i - r * 4 * KS);
-                u32x4_t a, b;
-                load_h<4>(p, r < count && k < p.r, m0 + r, k, sc, a, b);
-                *(u32x4_t *)(h_hi + r * H_PITCH + 2 * k) = a;
-                *(u32x4_t *)(h_lo + r * H_PITCH + 2 * k) = b;
+                f32x4_t x, y;
+                load_h<4>(p, r < count && k < p.r, m0 + r, k, sc, x, y);
+                *(f32x4_t *)(hs + r * H_PITCH + 4 * k) = x;
+                *(f32x4_t *)(hs + r * H_PITCH + 4 * k + 16) = y;
             }
         }
         bf16x8_t fa[KS][NB];
@@ -327,14 +344,15 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
             if (delta) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
-                    const int at = (16 * b + fi) * H_PITCH + 2 * (32 * s + 8 * fg);
-                    const bf16x8_t h = *(const bf16x8_t *)(h_hi + at), l = *(const bf16x8_t *)(h_lo + at);
+                    const uint8_t *at = hs + (16 * b + fi) * H_PITCH + 4 * (32 * s + 8 * fg);
+                    f32x4_t x = *(const f32x4_t *)at, y = *(const f32x4_t *)(at + 16);
 #pragma unroll
-                    for (int j = 0; j < NB; ++j)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h, acc[j], 0, 0, 0);
+                    for (int d = 0; d < 3; ++d) {
+                        const bf16x8_t h = take_bf16(x, y);
 #pragma unroll
-                    for (int j = 0; j < NB; ++j)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], l, acc[j], 0, 0, 0);
+                        for (int j = 0; j < NB; ++j)
+                            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h, acc[j], 0, 0, 0);
+                    }
                 }
             }
             // (LDS operations of a wave are done in order: no wait between them)

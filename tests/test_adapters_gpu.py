@@ -1,0 +1,60 @@
+"""lora_add where its middle activations are at the edges of their types."""
+import pytest
+import torch
+
+import tensor_bf16_gemm_amd as gc
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def randn(g, *shape, scale=1.0):
+    return (torch.randn(shape, generator=g) * scale).bfloat16()
+
+
+def run(base, X, down, up, scale, ids, out=None):
+    off, rows, _ = gc.group_rows(ids.to(DEV), down.shape[0])
+    d = [t.to(DEV) for t in (base, X, down, up, scale)]
+    return gc.lora_add(*d, off, rows, out=d[0] if out == "base" else out)
+
+
+def pieces(a):
+    """The bits 23..16, 15..8 and 7..0 of whole numbers below 2^24: each exact in bf16."""
+    return a & 0xFF0000, a & 0xFF00, a & 0xFF
+
+
+# (rows, adapters): few rows per adapter, and many
+@pytest.mark.parametrize("M,G", [(1, 1), (40, 5), (150, 2), (70, 1)])
+@pytest.mark.parametrize("r", [8, 16, 40, 72, 104, 128])
+def test_middle_sums_keep_all_bits(M, G, r):
+    """H holds pairs of a 24-bit number and the same with its low byte cleared, which up subtracts:
+    the low bytes are left, exactly.  Every fp32 sum on the way is a whole number below 2^24 times
+    a power of two, so the only rounding is that of the output."""
+    g = gen(M + r)
+    N, pairs = 136, r // 2
+    K = (3 * pairs + 7) // 8 * 8
+    a = torch.randint(1 << 23, 1 << 24, (M, pairs), generator=g)
+    X, down = torch.zeros(M, K), torch.zeros(G, K, r)
+    for p in range(pairs):
+        for i, part in enumerate(pieces(a[:, p])):
+            X[:, 3 * p + i] = part.float()
+            down[:, 3 * p + i, 2 * p] = 1.0
+            if i < 2:
+                down[:, 3 * p + i, 2 * p + 1] = 1.0
+    up = torch.zeros(G, r, N)
+    up[:, 0::2], up[:, 1::2] = 1.0, -1.0
+    up[:, :, 1::3] *= 0.5
+    scale = torch.tensor([2.0 ** -(i % 3) for i in range(G)])
+    ids = torch.randint(0, G, (M,), generator=g, dtype=torch.int32)
+    log(f"whole middle sums M={M} G={G} r={r}")
+    got = run(torch.zeros(M, N).bfloat16(), X.bfloat16(), down.bfloat16(), up.bfloat16(), scale, ids)
+    low = (a & 0xFF).sum(1).double()
+    want = (low * scale[ids.long()].double())[:, None] * up[0, 0].double()
+    assert torch.equal(got.cpu(), want.bfloat16())
