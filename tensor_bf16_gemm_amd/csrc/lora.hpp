@@ -102,6 +102,18 @@ __device__ __forceinline__ bf16x8_t take_bf16(f32x4_t &x, f32x4_t &y)
     return __builtin_bit_cast(bf16x8_t, r);
 }
 
+// The product of the leading parts plus that of the rests.  Where H or up holds
+// infinities the first alone is what the whole product is (its parts have the
+// signs of their values), while the rest is inf - inf or 0 * inf.
+__device__ __forceinline__ f32x4_t whole_product(f32x4_t lead, f32x4_t rest)
+{
+    f32x4_t s = lead + rest;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        s[i] = s[i] == s[i] ? s[i] : lead[i];
+    return s;
+}
+
 // Workgroups that a CU holds at once (their blocks of up fill its LDS).
 constexpr int expand_resident(int steps) { return steps == 1 ? 3 : steps <= 3 ? 2 : 1; }
 
@@ -191,10 +203,10 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
         for (int n0 = n_begin; n0 < n_end; n0 += EX_COLS) {
             wait_vmcnt<0>();                     // this wave's part of the block of up has landed,
             __syncthreads();                     // now everybody's
-            f32x4_t acc[4];
+            f32x4_t acc[4], rest[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+                acc[j] = rest[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < KS; ++s)
 #pragma unroll
@@ -207,14 +219,15 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
                     bf16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4bf16(
                         (lds_bf16x4_t *)lds_ptr<bf16x4_t>(a + 4 * 512));
                     const bf16x8_t fa = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s][0], acc[j], 0, 0, 0);
 #pragma unroll
-                    for (int d = 0; d < 3; ++d)
-                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s][d], acc[j], 0, 0, 0);
+                    for (int d = 1; d < 3; ++d)
+                        rest[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa, h[s][d], rest[j], 0, 0, 0);
                 }
             // (LDS operations of a wave are done in order: no wait between them)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = acc[j];
+                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = whole_product(acc[j], rest[j]);
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -337,28 +350,32 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 next[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(b + 1, i), 0, 0);
-            f32x4_t acc[NB];
+            f32x4_t acc[NB], rest[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+                acc[j] = rest[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
             if (delta) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s) {
                     const uint8_t *at = hs + (16 * b + fi) * H_PITCH + 4 * (32 * s + 8 * fg);
                     f32x4_t x = *(const f32x4_t *)at, y = *(const f32x4_t *)(at + 16);
+                    const bf16x8_t h = take_bf16(x, y);
 #pragma unroll
-                    for (int d = 0; d < 3; ++d) {
-                        const bf16x8_t h = take_bf16(x, y);
+                    for (int j = 0; j < NB; ++j)
+                        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h, acc[j], 0, 0, 0);
+#pragma unroll
+                    for (int d = 1; d < 3; ++d) {
+                        const bf16x8_t l = take_bf16(x, y);
 #pragma unroll
                         for (int j = 0; j < NB; ++j)
-                            acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], h, acc[j], 0, 0, 0);
+                            rest[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[s][j], l, rest[j], 0, 0, 0);
                     }
                 }
             }
             // (LDS operations of a wave are done in order: no wait between them)
 #pragma unroll
             for (int j = 0; j < NB; ++j)
-                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = acc[j];
+                *(f32x4_t *)(ex + fi * PITCH + (16 * j + 4 * fg) * 4) = whole_product(acc[j], rest[j]);
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -1,12 +1,16 @@
 """lora_add where its middle activations are at the edges of their types."""
+import math
+
 import pytest
 import torch
 
+import grouped_ref as ref
 import tensor_bf16_gemm_amd as gc
 from gpu_util import log
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+INF = math.inf
 
 
 def gen(seed):
@@ -58,3 +62,41 @@ def test_middle_sums_keep_all_bits(M, G, r):
     low = (a & 0xFF).sum(1).double()
     want = (low * scale[ids.long()].double())[:, None] * up[0, 0].double()
     assert torch.equal(got.cpu(), want.bfloat16())
+
+
+@pytest.mark.parametrize("M,G", [(12, 2), (90, 2)])
+@pytest.mark.parametrize("r", [8, 64, 96])
+def test_infinite_and_largest_middle_sums(M, G, r):
+    """An infinite H, one that lies above the largest bf16, and infinite and NaN weights give what
+    the sum in 64 bits gives, in their own rows and columns only."""
+    g = gen(M * r)
+    K, N = 72, 200
+    X, base = randn(g, M, K), randn(g, M, N)
+    down, up = randn(g, G, K, r, scale=K ** -0.5), randn(g, G, r, N, scale=r ** -0.5)
+    X[:, :8] = 0.0
+    down[:, :8] = 0.0
+    down[:, 3] = 1.0                                    # X[.., 3] reaches every middle value
+    down[:, 5:8, 0] = 1.0                               # X[.., 5:8] the first one alone
+    down[:, 5:8, 1:] = 0.0
+    up[:, :, :100] = up[:, :, :100].abs() + 2.0 ** -10  # an infinite H gives inf here, NaN among the others
+    ids = torch.arange(M, dtype=torch.int32) % G
+    X[2, 3], X[5, 3], X[M - 1, 3] = INF, -INF, math.nan
+    # 2^128 - 2^118: finite, and nearer to 2^128 than to the largest bf16; the adapter's products
+    # with it stay finite (the rest of the row is zero)
+    big = torch.tensor([2.0 ** 128 - 2.0 ** 120, 2.0 ** 119, 2.0 ** 118], dtype=torch.float64).bfloat16()
+    X[6] = 0.0
+    X[6, 5:8] = big
+    up[:, 0] = up[:, 0].abs().clamp(0.01, 0.5)
+    up[1, 1, 150], up[1, 2, 151], up[1, 3, 152] = INF, -INF, math.nan
+    scale = torch.tensor([1.0, 0.5])
+    want, tol = ref.lora(base, X, down, up, scale, ids)
+    log(f"infinite middle sums M={M} r={r}")
+    for out in (None, "base"):
+        got = run(base, X, down, up, scale, ids, out).cpu().double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        odd = torch.isinf(want)
+        assert torch.equal(got[odd], want[odd])
+        ok = torch.isfinite(want)
+        # fp32 sums of an adapter with an infinite weight have no bound; their finite ones do
+        assert torch.all((got - want).abs()[ok] <= tol[ok])
+    assert odd[2, :100].all() and odd[5, :100].all() and ok[6].all()
