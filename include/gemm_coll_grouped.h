@@ -90,7 +90,9 @@ int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int
 
 /*
  * Grouping of the ids [T][k] (a row is item / k) into `groups` groups; an id
- * outside [0, groups) is in none.  Sizes and workspace as moe_route.
+ * outside [0, groups) is in none.  1 <= groups <= 1024, k >= 1 of any size,
+ * T * k <= 2^24 (GC_ENOTSUP beyond).  More than 1024 ids need the workspace
+ * (GC_EINVAL without).
  */
 int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32_t *offsets,
                          int32_t *rows, int32_t *slots, void *workspace, uint64_t workspace_bytes,

@@ -358,6 +358,7 @@ int gemm_coll_moe_route(const void *logits, int logits_type, int64_t stride, int
     a.T = (int)T;
     a.E = E;
     a.k = k;
+    a.per_row = k;
     a.score = score;
     a.renorm = renormalize != 0;
     a.scale = scale;
@@ -380,10 +381,12 @@ int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32
         return GC_ENOTSUP;
     if (T > 0 && (!good4(ids) || !good4(rows) || !good4(slots)))
         return GC_EINVAL;
+    // (Blocks are of items, not of rows, which may be longer than a block.)
     gc::RouteArgs a = {};
-    a.T = (int)T;
+    a.T = (int)T * k;
     a.E = groups;
-    a.k = k;
+    a.k = 1;
+    a.per_row = k;
     a.ids = const_cast<int32_t *>(ids);      // (only read: no routing)
     a.offsets = offsets;
     a.rows = rows;

@@ -51,12 +51,13 @@ struct RouteArgs {
     const void *logits;      // [T] rows of E, row stride `stride` elements
     int64_t stride;
     const float *bias;       // [E] or null
-    int T, E, k;
+    int T, E, k;             // (grouping alone: T items, k = 1)
     int score, renorm;
     float scale;
     int32_t *ids;            // [T][k]
     float *weights;          // [T][k]
     // grouping (null offsets: none)
+    int per_row;             // items of a row
     int32_t *offsets;        // [E + 1]
     int32_t *rows;           // [T * k]
     int32_t *slots;          // [T * k]
@@ -459,7 +460,7 @@ __device__ __forceinline__ int counts_to_positions(GroupLds &l, int waves, int e
 
 __device__ __forceinline__ void place(const RouteArgs &p, int flat, int g, int pos)
 {
-    p.rows[pos] = (int)((unsigned)flat / (unsigned)p.k);
+    p.rows[pos] = (int)((unsigned)flat / (unsigned)p.per_row);
     p.slots[flat] = g == p.E ? -1 : pos;
 }
 
