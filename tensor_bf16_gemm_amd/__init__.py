@@ -16,12 +16,18 @@ Tensors are bf16, contiguous, on the current CUDA (HIP) device.  By default
 each call uses a workspace that lets the kernel split leftover tiles along
 K, allocated once per (device, stream) pair, so that calls in flight on
 different streams never share one; pass workspace=False to compute every
-tile whole, or a zero-filled uint8 tensor of workspace_bytes() of your own.  A failed
+tile whole, or a zero-filled uint8 tensor of workspace_bytes() of your own.  With stream= a
+call runs on that stream, and the caller orders it after what wrote its
+inputs and before what reads its output.  A new output comes from that
+stream's memory, and with a torch stream the tensors of the call may be
+dropped at once; with a raw handle the caller keeps them until the work is
+done.  A failed
 call raises RuntimeError with the library's message.  If the library is not
 built, the first call raises: there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -224,17 +230,52 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _side(stream):
+    """`stream` as a torch stream where it is not the current one, else None."""
+    if stream is None:
+        return None
+    import torch
+    handle = _stream(stream)
+    if handle == torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice()):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+
+
+def _empty(shape, like, stream):
+    """A new bf16 output beside `like` of a call on `stream`, from that stream's memory: what the
+    current stream has freed may still be in use there."""
+    import torch
+    side = _side(stream)
+    with torch.cuda.stream(side) if side is not None else contextlib.nullcontext():
+        out = torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if side is not None:
+        out.record_stream(torch.cuda.current_stream())
+    return out
+
+
+def _hold(stream, *tensors):
+    """Keeps the memory of the tensors of a call on another torch stream from being used again
+    before that stream is through with them.  (A raw handle may be gone by then: there the caller
+    does.)"""
+    side = _side(stream)
+    if side is not None and side is stream:
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(side)
+
+
 def gemm_ar(A, B, partials, out=None, *, R: int, rank: int, stream=None, workspace=None,
             status=None, tile_rows: int = 0, split_wait_spins: int = 0):
     """GEMM-AR: out [M,N] = bf16(A.B + sum of partials [R-1,M,N])."""
-    import torch
     M, K = A.shape
     N = B.shape[1]
     _bf16("A", A)
     _bf16("B", B, (K, N))
     _bf16("partials", partials, (R - 1, M, N))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((M, N), A, stream)
     _bf16("out", out, (M, N))
     wp, wb = _ws_fields(workspace, A.device, stream)
     peers = GcPeers(partials=_ptr(partials), workspace=wp, workspace_bytes=wb,
@@ -242,6 +283,7 @@ def gemm_ar(A, B, partials, out=None, *, R: int, rank: int, stream=None, workspa
                     split_wait_spins=int(split_wait_spins))
     _check(lib().gemm_ar(_ptr(A), _ptr(B), M, N, K, R, rank, ctypes.byref(peers), _ptr(out),
                          _stream(stream)), "gemm_ar")
+    _hold(stream, A, B, partials, out, status)
     return out
 
 
@@ -261,6 +303,7 @@ def gemm_ar_noalloc(A, B, partials, out, *, R: int, rank: int, stream=None, stat
     peers = GcPeers(partials=_ptr(partials), status=_ptr(status), tile_rows=int(tile_rows))
     _check(lib().gemm_ar_noalloc(_ptr(A), _ptr(B), M, N, K, R, rank, ctypes.byref(peers),
                                  _ptr(out), _stream(stream)), "gemm_ar_noalloc")
+    _hold(stream, A, B, partials, out, status)
     return out
 
 
@@ -268,7 +311,6 @@ def gemm_rs(A, B, partials, ws, out=None, *, R: int, rank: int, stream=None, wor
             status=None, tile_rows: int = 0, split_wait_spins: int = 0):
     """GEMM-RS: out [ceil(M/R), N] = this rank's rows of bf16(A.B + sum of partials);
     ws [M,N] receives bf16(A.B) on the rows this rank does not own."""
-    import torch
     M, K = A.shape
     N = B.shape[1]
     P = (M + R - 1) // R
@@ -277,7 +319,7 @@ def gemm_rs(A, B, partials, ws, out=None, *, R: int, rank: int, stream=None, wor
     _bf16("partials", partials, (R - 1, M, N))
     _bf16("ws", ws, (M, N))
     if out is None:
-        out = torch.empty((P, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((P, N), A, stream)
     _bf16("out", out, (P, N))
     wp, wb = _ws_fields(workspace, A.device, stream)
     peers = GcPeers(partials=_ptr(partials), ws=_ptr(ws), workspace=wp, workspace_bytes=wb,
@@ -285,6 +327,7 @@ def gemm_rs(A, B, partials, ws, out=None, *, R: int, rank: int, stream=None, wor
                     split_wait_spins=int(split_wait_spins))
     _check(lib().gemm_rs(_ptr(A), _ptr(B), M, N, K, R, rank, ctypes.byref(peers), _ptr(out),
                          _stream(stream)), "gemm_rs")
+    _hold(stream, A, B, partials, ws, out, status)
     return out
 
 
@@ -294,7 +337,6 @@ def gemm_ar_two_shot(A, B, partials, ws, peer_out, out=None, *, R: int, rank: in
     bf16(A.B + sum of partials) go to out [M,N] and to every slot of
     peer_out [R-1,M,N]; ws [M,N] receives bf16(A.B) on the other rows.  Rows
     of out and peer_out outside the slice are left untouched."""
-    import torch
     M, K = A.shape
     N = B.shape[1]
     _bf16("A", A)
@@ -303,7 +345,7 @@ def gemm_ar_two_shot(A, B, partials, ws, peer_out, out=None, *, R: int, rank: in
     _bf16("ws", ws, (M, N))
     _bf16("peer_out", peer_out, (R - 1, M, N))
     if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((M, N), A, stream)
     _bf16("out", out, (M, N))
     wp, wb = _ws_fields(workspace, A.device, stream)
     peers = GcPeers(partials=_ptr(partials), ws=_ptr(ws), workspace=wp, workspace_bytes=wb,
@@ -311,6 +353,7 @@ def gemm_ar_two_shot(A, B, partials, ws, peer_out, out=None, *, R: int, rank: in
                     split_wait_spins=int(split_wait_spins))
     _check(lib().gemm_ar_two_shot(_ptr(A), _ptr(B), M, N, K, R, rank, ctypes.byref(peers),
                                   _ptr(out), _stream(stream)), "gemm_ar_two_shot")
+    _hold(stream, A, B, partials, ws, peer_out, out, status)
     return out
 
 
@@ -320,7 +363,6 @@ def ag_gemm(A, B, shards, flags, status, out=None, *, R: int, rank: int, epoch: 
     """AG-GEMM: out [R*Ms, N] = bf16(concat(shards).B), A = this rank's shard [Ms,K].
     flags: int32 tensor [R] in device memory or pinned host memory (the kernel
     polls it with system-scope loads); status: int32 device tensor [1]."""
-    import torch
     Ms, K = A.shape
     N = B.shape[1]
     _bf16("A", A)
@@ -332,7 +374,7 @@ def ag_gemm(A, B, shards, flags, status, out=None, *, R: int, rank: int, epoch: 
     if status.numel() < 1 or status.element_size() != 4 or not status.is_cuda:
         raise ValueError("status must be a 4-byte device tensor")
     if out is None:
-        out = torch.empty((R * Ms, N), dtype=torch.bfloat16, device=A.device)
+        out = _empty((R * Ms, N), A, stream)
     _bf16("out", out, (R * Ms, N))
     wp, wb = _ws_fields(workspace, A.device, stream)
     peers = GcPeers(shards=_ptr(shards), flags=_ptr(flags), epoch=int(epoch) & 0xFFFFFFFF,
@@ -341,6 +383,7 @@ def ag_gemm(A, B, shards, flags, status, out=None, *, R: int, rank: int, epoch: 
                     split_wait_spins=int(split_wait_spins))
     _check(lib().ag_gemm(_ptr(A), _ptr(B), Ms, N, K, R, rank, ctypes.byref(peers), _ptr(out),
                          _stream(stream)), "ag_gemm")
+    _hold(stream, A, B, shards, flags, status, out)
     return out
 
 
@@ -361,12 +404,13 @@ def peer_sum(local, partials, out=None, *, stream=None):
     if partials.shape[0] > 0 and rows * N > 0 and (partials.stride(2) != 1 or partials.stride(1) != N):
         raise ValueError("partials: rows must be contiguous")
     if out is None:
-        out = torch.empty((rows, N), dtype=torch.bfloat16, device=local.device)
+        out = _empty((rows, N), local, stream)
     _bf16("out", out, (rows, N))
     npeers = partials.shape[0]
     stride = partials.stride(0) if npeers > 0 else 0
     _check(lib().gemm_coll_peer_sum(_ptr(local), _ptr(partials) if npeers else None, rows, N, npeers,
                                     stride, _ptr(out), _stream(stream)), "gemm_coll_peer_sum")
+    _hold(stream, local, partials, out)
     return out
 
 
@@ -386,6 +430,7 @@ def ag_push_shards(src, dst, flags, epoch_word, *, R: int, rank: int, stream=Non
             raise ValueError(f"{name}: expected a 32-bit device tensor of shape ({n},)")
     _check(lib().ag_push_shards(_ptr(src), _ptr(dst), Ms, K, R, rank, _ptr(flags), _ptr(epoch_word),
                                 _stream(stream)), "ag_push_shards")
+    _hold(stream, src, dst, flags, epoch_word)
 
 
 _GROUPED = ("moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add", "Routing", "Groups",

@@ -10,7 +10,7 @@ include/gemm_coll_grouped.h.
     out = lora_add(out, x, down, up, scale, g.offsets, g.rows, out=out)
 
 Tensors are on the current CUDA (HIP) device; calls are asynchronous on the
-current stream (or ``stream=``).  Each (device, stream) pair gets its own
+current stream (or ``stream=``, as for the package's other calls).  Each (device, stream) pair gets its own
 workspace, allocated on first use; pass ``workspace=`` (a zero-filled uint8
 tensor) to use one of your own.
 
@@ -156,6 +156,21 @@ def _place(t, workspace, more: int = 0, stream=None):
     return st, *_workspace(workspace, st, more)
 
 
+def _on(stream, call, *args):
+    """call(*args) for a launch on `stream`.  On a stream that is not the current one the outputs
+    come from its memory, and the inputs' is kept until it is through with them."""
+    side = _gc._side(stream)
+    if side is None:
+        return call(*args)
+    with torch.cuda.stream(side):
+        r = call(*args)
+    here = torch.cuda.current_stream()
+    for t in r if isinstance(r, tuple) else (r,):
+        t.record_stream(here)
+    _gc._hold(stream, *(t for t in args if isinstance(t, torch.Tensor)))
+    return r
+
+
 def moe_route(logits, k: int, *, score: str = "softmax", bias=None, renormalize: bool = True,
               scale: float = 1.0, stream=None, workspace=None) -> Routing:
     """The k experts of largest logit (with ``bias`` [E]: of largest score + bias) for each row
@@ -165,15 +180,15 @@ def moe_route(logits, k: int, *, score: str = "softmax", bias=None, renormalize:
     ``renormalize``, times ``scale``.  The T*k pairs come back grouped by expert."""
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    return Routing._make(_native.moe_route(logits, k, _SCORES[score], bias, renormalize, scale,
-                                           *_place(logits, workspace, 0, stream)))
+    return Routing._make(_on(stream, _native.moe_route, logits, k, _SCORES[score], bias, renormalize, scale,
+                             *_place(logits, workspace, 0, stream)))
 
 
 def group_rows(ids, groups: int, *, stream=None, workspace=None) -> Groups:
     """Stable grouping of ids [T] or [T,k] (int32) into ``groups`` groups; ids outside
     [0, groups) are in none and come last.  rows[i] is the row (first index) of the item at
     position i, slots has the shape of ids."""
-    return Groups._make(_native.group_rows(ids, groups, *_place(ids, workspace, 0, stream)))
+    return Groups._make(_on(stream, _native.group_rows, ids, groups, *_place(ids, workspace, 0, stream)))
 
 
 def grouped_gemm(X, W, offsets, rows=None, out=None, *, act: str | None = None, stream=None,
@@ -183,14 +198,16 @@ def grouped_gemm(X, W, offsets, rows=None, out=None, *, act: str | None = None, 
     Positions in no group are left as they are.  workspace=False: no product is split along K."""
     if act not in _ACTS:
         raise ValueError(f"act must be None or 'silu_glu', got {act!r}")
-    return _native.grouped_gemm(X, W, offsets, rows, out, _ACTS[act], *_place(X, workspace, 0, stream))
+    return _on(stream, _native.grouped_gemm, X, W, offsets, rows, out, _ACTS[act],
+               *_place(X, workspace, 0, stream))
 
 
 def moe_combine(Y, slots, weights, partials=None, out=None, *, stream=None):
     """out [T,N] = bf16(sum over j of weights[t,j] * Y[slots[t,j]] + sum over p of partials[p,t]);
     slots outside Y (-1) are skipped.  partials [npeers,T,N] with contiguous rows; stride(0) may be
     larger (a row slice of every peer's partial, with the same slice of slots and weights)."""
-    return _native.moe_combine(Y, slots, weights, partials, out, _handle(stream) if Y.is_cuda else 0)
+    return _on(stream, _native.moe_combine, Y, slots, weights, partials, out,
+               _handle(stream) if Y.is_cuda else 0)
 
 
 def lora_add(base, X, down, up, scale, offsets, rows, out=None, *, stream=None, workspace=None):
@@ -198,5 +215,5 @@ def lora_add(base, X, down, up, scale, offsets, rows, out=None, *, stream=None, 
     adapter a's positions offsets[a] <= i < offsets[a+1] (group_rows of the rows' adapters), base[m]
     for rows of no adapter.  down [G,K,r], up [G,r,N], scale float32 [G]; out may be base."""
     sums = X.shape[0] * down.shape[-1]               # fp32, in the workspace
-    return _native.lora_add(base, X, down, up, scale, offsets, rows, out,
-                            *_place(X, workspace, 4 * sums if sums > 1 << 24 else 0, stream))
+    return _on(stream, _native.lora_add, base, X, down, up, scale, offsets, rows, out,
+               *_place(X, workspace, 4 * sums if sums > 1 << 24 else 0, stream))
