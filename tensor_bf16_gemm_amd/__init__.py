@@ -30,6 +30,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import threading
 
 __all__ = ["gemm_ar", "gemm_ar_noalloc", "gemm_rs", "gemm_ar_two_shot", "ag_gemm", "ag_push_shards", "peer_sum",
            "should_run", "strerror", "plan",
@@ -143,6 +144,7 @@ def plan(mode: str, M: int, N: int, K: int, R: int, rank: int = 0, *, cus: int =
 
 
 _workspaces: dict = {}
+_making = threading.Lock()          # held while a default workspace is made
 
 
 def workspace_bytes() -> int:
@@ -183,11 +185,13 @@ def default_workspace(device=None, stream=None):
 
 def _cached_workspace(key: tuple[int, int], make):
     """The workspace cached under key = (device, stream), made by make() on
-    first use."""
+    first use (by one thread; the others get the same)."""
     ws = _workspaces.get(key)
     if ws is None:
-        ws = make()
-        _workspaces[key] = ws
+        with _making:
+            ws = _workspaces.get(key)
+            if ws is None:
+                ws = _workspaces[key] = make()
     return ws
 
 

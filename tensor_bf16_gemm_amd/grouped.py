@@ -131,20 +131,26 @@ def _workspace(workspace, stream: int, more: int = 0) -> tuple[int | None, int]:
     key = (torch._C._cuda_getDevice(), stream)
     have = _scratch.get(key)
     if have is None or have[2] < more:
-        have = _new_scratch(key, have, more)
+        have = _new_scratch(key, more)
     return have[1], have[2] + _base_bytes[key[0]]
 
 
-def _new_scratch(key, have, more):
-    # Twice what is asked for, so that growing sizes replace it seldom; a
-    # replaced one stays allocated, for work in flight may still use it.
-    more = max(more, 2 * have[2]) if have else more
-    t = torch.zeros(grouped_workspace_bytes() + more, dtype=torch.uint8, device=f"cuda:{key[0]}")
-    torch.cuda.synchronize(key[0])
-    if have:
-        _kept.append(have[0])
-    _scratch[key] = (t, t.data_ptr(), more)
-    return _scratch[key]
+def _new_scratch(key, more):
+    # One thread at a time (the synchronization lets others run), and the next
+    # finds what this one has made.  At least twice the size of the one before,
+    # so that growing sizes replace it seldom; a replaced one stays allocated,
+    # for work in flight may still use it.
+    with _gc._making:
+        have = _scratch.get(key)
+        if have is not None and have[2] >= more:
+            return have
+        more = max(more, 2 * have[2]) if have else more
+        t = torch.zeros(grouped_workspace_bytes() + more, dtype=torch.uint8, device=f"cuda:{key[0]}")
+        torch.cuda.synchronize(key[0])
+        if have:
+            _kept.append(have[0])
+        _scratch[key] = (t, t.data_ptr(), more)
+        return _scratch[key]
 
 
 def _place(t, workspace, more: int = 0, stream=None):
