@@ -201,9 +201,22 @@ def _ws_fields(workspace, device, stream):
     device tensor."""
     if workspace is False:
         return None, 0
-    if workspace is None:
-        workspace = default_workspace(device, stream)
+    if workspace is not None:
+        return _own_workspace(workspace)
+    workspace = default_workspace(device, stream)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _own_workspace(t):
+    """(pointer, bytes) of a workspace tensor on the current device."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("workspace must be a device tensor")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"workspace is on {t.device}, not on the current device")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def _check(code: int, what: str):

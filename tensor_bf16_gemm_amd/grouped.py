@@ -127,7 +127,7 @@ def _workspace(workspace, stream: int, more: int = 0) -> tuple[int | None, int]:
     if workspace is False:
         return None, 0
     if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        return _gc._own_workspace(workspace)
     key = (torch._C._cuda_getDevice(), stream)
     have = _scratch.get(key)
     if have is None or have[2] < more:

@@ -79,3 +79,11 @@ def test_threads_share_the_projections_workspace(monkeypatch):
         return made[-1]
     got = at_once(lambda: gc._cached_workspace((0, 7), make))
     assert len(made) == 1 and all(w is made[0] for w in got)
+
+
+def test_workspaces_in_host_memory_are_refused():
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="device tensor"):
+        grouped._workspace(ws, 0)
+    with pytest.raises(ValueError, match="device tensor"):
+        gc._ws_fields(ws, None, 0)
