@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/impl/DeviceGuardImplInterface.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <string>
@@ -48,15 +49,26 @@ const Tensor &tensor(PyObject *o, const char *name)
     return THPVariable_Unpack(o);
 }
 
-// A contiguous device tensor of the given type.
+// Refuses a tensor that is not on the current device, whose stream the call
+// is launched on.
+void here(const Tensor &t, const char *name)
+{
+    if (!t.is_cuda())
+        refuse(PyExc_ValueError, std::string(name) + " must be a device tensor");
+    const auto now = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
+    if (t.device().index() != now)
+        refuse(PyExc_ValueError, std::string(name) + " is on " + t.device().str() +
+                                     ", the current device is cuda:" + std::to_string(now));
+}
+
+// A contiguous tensor of the given type on the current device.
 const Tensor &dense(PyObject *o, const char *name, at::ScalarType type)
 {
     const Tensor &t = tensor(o, name);
     if (t.scalar_type() != type)
         refuse(PyExc_TypeError, std::string(name) + " must be " + type_name(type) + ", got torch." +
                                     c10::toString(t.scalar_type()));
-    if (!t.is_cuda())
-        refuse(PyExc_ValueError, std::string(name) + " must be a device tensor");
+    here(t, name);
     if (!t.is_contiguous())
         refuse(PyExc_ValueError, std::string(name) + " must be contiguous");
     return t;
@@ -159,8 +171,7 @@ PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         if (x.dim() != 2 || (type != at::kFloat && type != at::kBFloat16))
             refuse(PyExc_TypeError, std::string("logits must be float32 or bfloat16 [T, E], got ") +
                                         c10::toString(type) + " " + text(x.sizes()));
-        if (!x.is_cuda())
-            refuse(PyExc_ValueError, "logits must be a device tensor");
+        here(x, "logits");
         const int64_t T = x.size(0), E = x.size(1);
         const int k = small(a[1], "k");
         if (E > 1 && T > 0 && x.stride(1) != 1)
@@ -278,6 +289,7 @@ PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t nargs)
                                              std::to_string(N) + "], got " + c10::toString(p.scalar_type()) +
                                              " " + text(p.sizes()));
             if (p.size(0) > 0) {
+                // (on another device too, where this one can reach its memory)
                 if (!p.is_cuda())
                     refuse(PyExc_ValueError, "partials must be a device tensor");
                 if (T * N > 0 && (p.stride(2) != 1 || (T > 1 && p.stride(1) != N)))
