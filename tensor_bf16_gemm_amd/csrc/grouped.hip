@@ -100,10 +100,11 @@ void launch_route(const gc::RouteArgs &a, int blocks, hipStream_t st)
 int route_and_group(gc::RouteArgs &a, bool route, bool bf16, void *workspace, uint64_t bytes,
                     hipStream_t st)
 {
-    // One workgroup for everything: up to two tokens for each row of lanes.
+    // One workgroup for everything: up to two tokens for each row of lanes, and
+    // more where there is no workspace for more workgroups.
     const int64_t items = (int64_t)a.T * a.k;
     const int at_once = gc::RT_THREADS / route_lanes(a.E);
-    if (items <= gc::ROUTE_ONE_ITEMS && (!route || a.T <= 2 * at_once)) {
+    if (items <= gc::ROUTE_ONE_ITEMS && (!route || a.T <= 2 * at_once || (a.offsets && !workspace))) {
         if (!route)
             hipLaunchKernelGGL((gc::route_kernel<16, 0, false, true>), dim3(1), dim3(gc::RT_THREADS), 0, st, a);
         else if (bf16)

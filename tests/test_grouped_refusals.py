@@ -23,3 +23,11 @@ def test_group_rows_of_wide_rows(T, k):
     code = ("import tensor_bf16_gemm_amd as gc; P = 0x7F0000000000; "
             f"print(gc.lib().gemm_coll_group_rows(P, {T}, {k}, 8, P, P, P, None, 0, None))")
     assert in_a_process(code) == str(gc.GC_EINVAL)
+
+
+@pytest.mark.parametrize("T,E,k", [(129, 64, 8), (1025, 64, 1), (342, 300, 3), (65, 8, 16)])
+def test_more_than_1024_pairs_need_the_workspace(T, E, k):
+    P = 0x7F0000000000
+    L = gc.lib()
+    assert L.gemm_coll_moe_route(P, 0, E, T, E, k, 0, None, 1, 1.0, P, P, P, P, P, None, 0, None) == gc.GC_EINVAL
+    assert L.gemm_coll_group_rows(P, T, k, E, P, P, P, None, 0, None) == gc.GC_EINVAL

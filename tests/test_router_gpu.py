@@ -25,3 +25,25 @@ def test_group_rows_of_wide_rows(T, k, groups):
     for got, want, name in zip(gc.group_rows(ids.to(DEV), groups), ref.group(ids, groups),
                                ("offsets", "rows", "slots")):
         assert torch.equal(got.cpu(), want), name
+
+
+def check_routing(logits, k, workspace=None, **kw):
+    T, E = logits.shape
+    log(f"route T={T} E={E} k={k} {logits.dtype} workspace={workspace}")
+    r = gc.moe_route(logits.to(DEV), k, workspace=workspace, **kw)
+    ids, w = ref.route(logits, k, **kw)
+    assert torch.equal(r.ids.cpu(), ids)
+    # exp and the division: a few units; x - max rounds by |x - max| u; the sum by E u
+    bound = (2 * float(logits.float().abs().max()) + E + 32) * 2 * ref.U
+    assert torch.all((r.weights.cpu().double() - w).abs() <= bound * w.abs() + 1e-37)
+    for got, want, name in zip((r.offsets, r.rows, r.slots), ref.group(ids, E), ("offsets", "rows", "slots")):
+        assert torch.equal(got.cpu(), want), name
+
+
+@pytest.mark.parametrize("T,E,k", [(129, 64, 1), (1024, 20, 1), (33, 257, 8), (341, 300, 3), (146, 5, 7)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_without_workspace(T, E, k, dtype):
+    """More tokens than one workgroup routes at a time, in one workgroup."""
+    logits = (torch.randn((T, E), generator=gen(T)) * 2).to(dtype)
+    check_routing(logits, k, workspace=False)
+    check_routing(logits, k, score="sigmoid")
