@@ -116,7 +116,7 @@ def lib() -> ctypes.CDLL:
                                      ctypes.c_int, ctypes.c_int, ctypes.c_uint32,
                                      ctypes.POINTER(GcPlan)]
         L.gemm_coll_plan.restype = ctypes.c_int
-        from .grouped import declare
+        from .grouped_abi import declare
         declare(L)
         _lib = L
     return _lib

@@ -54,35 +54,56 @@ def binding_flags() -> tuple[list[str], list[str]]:
             [f"-L{at}/lib", "-lc10", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
 
 
-def _run(cmds: list[list[str]]):
-    """Runs the commands side by side; raises with the output of the first that failed."""
-    runs = [(c, subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True))
-            for c in cmds]
-    for cmd, p in [(c, (p, p.communicate()[0])) for c, p in runs]:
-        if p[0].returncode != 0:
-            raise RuntimeError(f"build failed:\n{' '.join(cmd)}\n{p[1]}")
+def _start(cmd: list[str]):
+    return cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+
+
+def _wait(runs):
+    """Waits for the commands that run side by side; raises with the output of the first that failed."""
+    for cmd, p, text in [(c, p, p.communicate()[0]) for c, p in runs]:
+        if p.returncode != 0:
+            raise RuntimeError(f"build failed:\n{' '.join(cmd)}\n{text}")
+
+
+def _compile_binding(tmp: str):
+    """The running compilation of the binding, or why there is none (no g++, no PyTorch)."""
+    try:
+        return _start(["g++", *binding_flags()[0], "-c", "-o", os.path.join(tmp, "binding.o"),
+                       os.path.join(CSRC, "binding.cpp")])
+    except (ImportError, OSError) as e:
+        return e
+
+
+def _link_binding(run, tmp: str):
+    if isinstance(run, Exception):
+        raise RuntimeError(f"{LIB} is built, its binding {NATIVE} is not: {run}") from run
+    _wait([run])
+    native = os.path.join(tmp, "_native.so")
+    _wait([_start(["g++", "-shared", "-o", native, os.path.join(tmp, "binding.o"), f"-L{PKG}",
+                   "-l:libgemm_coll.so", *binding_flags()[1]])])
+    os.replace(native, NATIVE)
 
 
 def build(out_path: str = LIB, extra: tuple[str, ...] = ()) -> str:
-    """Compile the library and, at its own place, the binding (always); returns the library's path."""
+    """Compile the library and, at its own place, the binding (always); returns the library's path.
+    The library is in place before the binding is asked for: it needs neither g++ nor PyTorch, and
+    neither does what the package does without tensors."""
     with tempfile.TemporaryDirectory(dir=os.path.dirname(out_path)) as tmp:
-        objs = [os.path.join(tmp, name + ".o") for name in SOURCES]
-        cmds = [[hipcc(), *compile_flags(), "-c", *extra, "-o", o, os.path.join(CSRC, name)]
-                for o, name in zip(objs, SOURCES)]
-        binding = out_path == LIB
-        if binding:
-            flags, libs = binding_flags()
-            cmds.append(["g++", *flags, "-c", "-o", os.path.join(tmp, "binding.o"),
-                         os.path.join(CSRC, "binding.cpp")])
-        _run(cmds)
-        lib = os.path.join(tmp, "libgemm_coll.so")
-        _run([[hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", lib, *objs]])
-        if binding:
-            native = os.path.join(tmp, "_native.so")
-            _run([["g++", "-shared", "-o", native, os.path.join(tmp, "binding.o"), f"-L{tmp}",
-                   "-l:libgemm_coll.so", *libs]])
-            os.replace(native, NATIVE)
-        os.replace(lib, out_path)
+        binding = _compile_binding(tmp) if out_path == LIB else None
+        try:
+            objs = [os.path.join(tmp, name + ".o") for name in SOURCES]
+            _wait([_start([hipcc(), *compile_flags(), "-c", *extra, "-o", o, os.path.join(CSRC, name)])
+                   for o, name in zip(objs, SOURCES)])
+            lib = os.path.join(tmp, "libgemm_coll.so")
+            _wait([_start([hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", lib, *objs])])
+            os.replace(lib, out_path)
+        except BaseException:
+            if isinstance(binding, tuple):
+                binding[1].kill()
+                binding[1].communicate()
+            raise
+        if binding is not None:
+            _link_binding(binding, tmp)
     return out_path
 
 
