@@ -1,0 +1,40 @@
+// deal.hpp -- how the work of the grouped products is dealt to workgroups:
+// whole-number arithmetic without memory, the same on the device and on the
+// host, so that a host program can check it for any number of workgroups.
+#pragma once
+
+#include <stdint.h>
+
+namespace gc {
+
+// Tiles of many rows: unit t of queue x, in hands of `hand` units.
+constexpr int TK_QUEUES = 8;
+__host__ __device__ __forceinline__ int queue_unit(int x, int t, int hand)
+{
+    return (t / hand * TK_QUEUES + x) * hand + t % hand;
+}
+
+// The units of workgroup b of G where there are no tickets to draw: workgroups
+// x, x + 8, ... share queue x in turn; where there are fewer workgroups than
+// queues, each takes several queues whole.
+struct Share {
+    int queue, next, step, skip;
+    __host__ __device__ __forceinline__ Share(int b, int G)
+        : queue(b % TK_QUEUES), next(b / TK_QUEUES), step((G - b % TK_QUEUES + TK_QUEUES - 1) / TK_QUEUES),
+          skip(G < TK_QUEUES ? G : TK_QUEUES)
+    {
+    }
+    // The next unit below `units`, or -1.
+    __host__ __device__ __forceinline__ int draw(int hand, int units)
+    {
+        for (; queue < TK_QUEUES; queue += skip, next = 0) {
+            const int u = queue_unit(queue, next, hand);
+            next += step;
+            if (u < units)
+                return u;
+        }
+        return -1;
+    }
+};
+
+}  // namespace gc

@@ -38,11 +38,12 @@
 // the stores (65536 rows, N 7168: 717 of 860 us are left without them).
 #pragma once
 
+#include "deal.hpp"
 #include "grouped.hpp"
 
 namespace gc {
 
-constexpr int TK_QUEUES = 8, TK_GROUP_M = 6, TK_HAND = 64;
+constexpr int TK_GROUP_M = 6, TK_HAND = 64;
 // Counters of a launch, zero between launches: one ticket per queue (64 bytes
 // apart), and the workgroups that are through.
 constexpr int TK_TICKET_STRIDE = 16, TK_DONE = TK_QUEUES * TK_TICKET_STRIDE;
@@ -270,22 +271,16 @@ __global__ __launch_bounds__(NT, 2) void tile_kernel(GroupedArgs p)
     // where they are few: 8 groups of 512 rows, K 7168, N 1792 on two queues
     // took 305 us, on eight 122).
     const int hand = max(min(TK_HAND, (units + TK_QUEUES - 1) / TK_QUEUES), 1);
-    int x = blockIdx.x & (TK_QUEUES - 1), tried = 0, mine = blockIdx.x / TK_QUEUES;
-    const int per_queue = (G + TK_QUEUES - 1) / TK_QUEUES;
+    int x = blockIdx.x & (TK_QUEUES - 1), tried = 0;
+    Share share(blockIdx.x, G);
     // Next unit for this workgroup, or -1 (thread 0 only).
     auto draw = [&]() {
+        if (!p.count)                           // no workspace
+            return share.draw(hand, units);
         for (; tried < TK_QUEUES; ++tried, x = (x + 1) & (TK_QUEUES - 1)) {
-            int t;
-            if (p.count) {
-                t = (int)__hip_atomic_fetch_add(p.count + x * TK_TICKET_STRIDE, 1u, __ATOMIC_RELAXED,
-                                                __HIP_MEMORY_SCOPE_AGENT);
-            } else {                            // no workspace: equal shares
-                if (tried > 0)
-                    break;
-                t = mine;
-                mine += per_queue;
-            }
-            t = (t / hand * TK_QUEUES + x) * hand + t % hand;
+            const int t = queue_unit(x, (int)__hip_atomic_fetch_add(p.count + x * TK_TICKET_STRIDE, 1u,
+                                                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT),
+                                     hand);
             if (t < units)
                 return t;
         }
