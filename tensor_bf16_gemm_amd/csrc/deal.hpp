@@ -7,6 +7,16 @@
 
 namespace gc {
 
+// Sums of tiles stop here.  Offsets that fall, which no grouping has, can make
+// the groups' tiles more than an int counts (512 groups of 2^27 rows each);
+// the sums then stand still, and the tiles past them are left out.
+constexpr int MOST_TILES = 1 << 30;
+__host__ __device__ __forceinline__ int add_tiles(int a, int b)
+{
+    const uint32_t s = (uint32_t)a + (uint32_t)b;
+    return s < (uint32_t)MOST_TILES ? (int)s : MOST_TILES;
+}
+
 // Tiles of many rows: unit t of queue x, in hands of `hand` units.
 constexpr int TK_QUEUES = 8;
 __host__ __device__ __forceinline__ int queue_unit(int x, int t, int hand)

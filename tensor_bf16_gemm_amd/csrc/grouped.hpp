@@ -26,6 +26,7 @@
 // 53 us, tiles of 256 columns 51, a ring of 3 steps the same 46.)
 #pragma once
 
+#include "deal.hpp"
 #include "gc_kernel.hpp"
 
 namespace gc {
@@ -61,7 +62,8 @@ __device__ __forceinline__ void group_range(const int32_t *offsets, int E, int S
     hi = e < E ? min(max(offsets[e + 1], lo), S) : S;
 }
 
-// first[i] = the sum of count(0 .. i - 1), i = 0 .. n; returns the whole sum.
+// first[i] = the sum of count(0 .. i - 1), i = 0 .. n (by add_tiles, so that it
+// never falls); returns the whole sum.
 // NTH threads; n <= 1024.
 template <int NTH, class F>
 __device__ __forceinline__ int scan_counts(int n, F &&count, int *first, int *wsum)
@@ -73,29 +75,31 @@ __device__ __forceinline__ int scan_counts(int n, F &&count, int *first, int *ws
     for (int i = 0; i < PER; ++i) {
         const int at = PER * tid + i;
         c[i] = at < n ? count(at) : 0;
-        sum += c[i];
+        sum = add_tiles(sum, c[i]);
     }
     int inc = sum;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
         const int o = __shfl_up(inc, d);
         if (lane >= d)
-            inc += o;
+            inc = add_tiles(inc, o);
     }
     if (lane == 63)
         wsum[wave] = inc;
+    const int prev = __shfl_up(inc, 1);
     __syncthreads();
-    int at = inc - sum, all = 0;
+    int at = lane > 0 ? prev : 0, before = 0, all = 0;
     for (int w = 0; w < NTH / 64; ++w) {
         if (w < wave)
-            at += wsum[w];
-        all += wsum[w];
+            before = add_tiles(before, wsum[w]);
+        all = add_tiles(all, wsum[w]);
     }
+    at = add_tiles(before, at);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         if (PER * tid + i < n)
             first[PER * tid + i] = at;
-        at += c[i];
+        at = add_tiles(at, c[i]);
     }
     if (tid == 0)
         first[n] = all;

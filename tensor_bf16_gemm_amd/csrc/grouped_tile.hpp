@@ -38,7 +38,6 @@
 // the stores (65536 rows, N 7168: 717 of 860 us are left without them).
 #pragma once
 
-#include "deal.hpp"
 #include "grouped.hpp"
 
 namespace gc {

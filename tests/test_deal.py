@@ -38,3 +38,43 @@ def test_shares_cover_every_unit_once(tmp_path, hand):
                 if (std::count(taken.begin(), taken.end(), 1) != units)
                     printf("G %d units %d\\n", G, units);
             }}""") == []
+
+
+@pytest.mark.parametrize("groups,S,bm", [(1024, (1 << 27) - 1, 16), (1024, 1 << 26, 16), (1000, 3000, 64),
+                                         (7, (1 << 27) - 1, 16), (1023, (1 << 27) - 1, 32)])
+def test_tiles_of_falling_offsets_stay_in_their_groups(tmp_path, groups, S, bm):
+    """Offsets 0, S, 0, S, ...: whatever the sum of the groups' tiles is, a tile's place in its group is
+    one that the group has.  (The prefix sum of the kernels, by threads, waves and the workgroup.)"""
+    assert run(tmp_path, f"""
+        const int n = {groups}, S = {S}, bm = {bm}, threads = 256, per = 1024 / threads;
+        auto count = [&](int e) {{ return e < n && e % 2 == 0 ? (S + bm - 1) / bm : 0; }};
+        std::vector<int> first(n + 1), inc(threads), wave(threads / 64, 0);
+        for (int t = 0; t < threads; ++t) {{
+            int sum = 0;
+            for (int i = 0; i < per; ++i)
+                sum = add_tiles(sum, count(per * t + i));
+            inc[t] = t % 64 ? add_tiles(inc[t - 1], sum) : sum;
+            if (t % 64 == 63)
+                wave[t / 64] = inc[t];
+        }}
+        int all = 0;
+        for (int w : wave)
+            all = add_tiles(all, w);
+        for (int t = 0; t < threads; ++t) {{
+            int before = 0;
+            for (int w = 0; w < t / 64; ++w)
+                before = add_tiles(before, wave[w]);
+            int at = add_tiles(before, t % 64 ? inc[t - 1] : 0);
+            for (int i = 0; i < per; ++i) {{
+                if (per * t + i < n)
+                    first[per * t + i] = at;
+                at = add_tiles(at, count(per * t + i));
+            }}
+        }}
+        first[n] = all;
+        const int64_t real = (int64_t)(n + 1) / 2 * ((S + bm - 1) / bm);
+        if (all != std::min<int64_t>(real, MOST_TILES))
+            printf("sum %d\\n", all);
+        for (int e = 0; e < n; ++e)
+            if (first[e + 1] < first[e] || first[e + 1] - first[e] > count(e))
+                printf("group %d from %d to %d\\n", e, first[e], first[e + 1]);""") == []
