@@ -17,6 +17,46 @@ __host__ __device__ __forceinline__ int add_tiles(int a, int b)
     return s < (uint32_t)MOST_TILES ? (int)s : MOST_TILES;
 }
 
+// Tiles of few rows: the K quads (4 steps of 32) of all tiles form one line,
+// which `pieces` workgroups take in equal pieces: piece w is [bound(w),
+// bound(w+1)).  A bound that would leave less than `least` quads of a tile on
+// one side moves to the tile's edge.
+struct Line {
+    int64_t quads;             // tiles * per_tile
+    int per_tile, pieces, least;
+    // `smallest` quads are worth a piece of a tile; a tile of fewer is a piece
+    // itself (never cut, and as many pieces as there are tiles).
+    __host__ __device__ __forceinline__ Line(int tiles, int quads_of_tile, int smallest, int most_pieces)
+    {
+        per_tile = quads_of_tile;
+        quads = (int64_t)tiles * per_tile;
+        least = smallest < per_tile ? smallest : per_tile;
+        const int64_t n = quads / least;
+        pieces = n < 1 ? 1 : n < most_pieces ? (int)n : most_pieces;
+    }
+    __host__ __device__ __forceinline__ int64_t bound(int w) const
+    {
+        int64_t b = quads * w / pieces;
+        const int r = (int)(b % per_tile);
+        if (r < least)
+            b -= r;
+        else if (per_tile - r < least)
+            b += per_tile - r;
+        return b;
+    }
+    // the piece that holds quad q (the last with bound <= q)
+    __host__ __device__ __forceinline__ int piece_of(int64_t q) const
+    {
+        const int64_t guess = q * pieces / quads;
+        int w = guess < pieces ? (int)guess : pieces - 1;
+        while (w + 1 < pieces && bound(w + 1) <= q)
+            ++w;
+        while (w > 0 && bound(w) > q)
+            --w;
+        return w;
+    }
+};
+
 // Tiles of many rows: unit t of queue x, in hands of `hand` units.
 constexpr int TK_QUEUES = 8;
 __host__ __device__ __forceinline__ int queue_unit(int x, int t, int hand)

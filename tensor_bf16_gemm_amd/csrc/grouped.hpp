@@ -151,34 +151,6 @@ __device__ __forceinline__ f32x4_t silu_mul(f32x4_t g, f32x4_t u)
     return (f32x4_t){silu(g[0]) * u[0], silu(g[1]) * u[1], silu(g[2]) * u[2], silu(g[3]) * u[3]};
 }
 
-// The line of K quads: piece w of G is [bound(w), bound(w+1)).  A bound that
-// would leave less than `least` quads of a tile on one side moves to the
-// tile's edge.
-struct Line {
-    int64_t quads;             // tiles * per_tile
-    int per_tile, pieces, least;
-    __device__ __forceinline__ int64_t bound(int w) const
-    {
-        int64_t b = quads * w / pieces;
-        const int r = (int)(b % per_tile);
-        if (r < least)
-            b -= r;
-        else if (per_tile - r < least)
-            b += per_tile - r;
-        return b;
-    }
-    // the piece that holds quad q (the last with bound <= q)
-    __device__ __forceinline__ int piece_of(int64_t q) const
-    {
-        int w = (int)min((int64_t)(pieces - 1), q * pieces / quads);
-        while (w + 1 < pieces && bound(w + 1) <= q)
-            ++w;
-        while (w > 0 && bound(w) > q)
-            --w;
-        return w;
-    }
-};
-
 constexpr int ST_THREADS = 256, ST_WAVES = 4;
 
 // NB, RB: 16-column and 16-position blocks of a tile; D: slots of a ring.
@@ -208,19 +180,15 @@ __global__ __launch_bounds__(ST_THREADS) void stream_kernel(GroupedArgs p)
     const int tiles = scan_tiles<ST_THREADS>(p.offsets, p.E, p.S, p.E, BM, p.tiles_n, first, starts, wsum);
     if (tiles <= 0)
         return;
-    Line line;
-    line.per_tile = max((KT + ST_WAVES - 1) / ST_WAVES, 1);
-    line.quads = (int64_t)tiles * line.per_tile;
-    line.least = p.min_quads;
-    line.pieces = G;
+    constexpr bool LINE = EPI != EPI_SUMS;
+    const Line line(tiles, max((KT + ST_WAVES - 1) / ST_WAVES, 1), LINE ? p.min_quads : 1,
+                    LINE ? min(G, p.part_slots / 2) : 1);
     int64_t q, q_end;
     int v = blockIdx.x;
     if constexpr (EPI == EPI_SUMS) {
         q = v;                                           // units: (tile, piece of K)
         q_end = (int64_t)tiles * p.splits;
     } else {
-        line.pieces = (int)min((int64_t)min(G, p.part_slots / 2),
-                               max((int64_t)1, line.quads / max(p.min_quads, 1)));
         if (v >= line.pieces)
             return;
         v = xcd_remap(v, line.pieces);

@@ -78,3 +78,31 @@ def test_tiles_of_falling_offsets_stay_in_their_groups(tmp_path, groups, S, bm):
         for (int e = 0; e < n; ++e)
             if (first[e + 1] < first[e] || first[e + 1] - first[e] > count(e))
                 printf("group %d from %d to %d\\n", e, first[e], first[e + 1]);""") == []
+
+
+@pytest.mark.parametrize("per_tile", [1, 2, 3, 4, 5, 7, 8, 9, 56])
+def test_line_is_cut_into_pieces(tmp_path, per_tile):
+    """The pieces follow one another over the whole line, no tile is cut with fewer than `least` quads on a
+    side, every quad is found in its piece, and tiles that are not worth cutting go to as many workgroups
+    as there are."""
+    assert run(tmp_path, f"""
+        const int per = {per_tile};
+        for (int G : {{1, 3, 64, 255, 256}})
+            for (int tiles : {{1, 2, 5, 63, 128, 255, 256, 257, 448, 1000}})
+                for (int smallest : {{4, per}}) {{
+                    const Line l(tiles, per, smallest, G);
+                    bool ok = l.pieces >= 1 && l.pieces <= G && l.bound(0) == 0 && l.bound(l.pieces) == (int64_t)tiles * per;
+                    int64_t longest = 0;
+                    for (int w = 0; w < l.pieces; ++w) {{
+                        const int64_t a = l.bound(w), b = l.bound(w + 1);
+                        const int r = (int)(b % per);
+                        ok &= a <= b && (r == 0 || (r >= smallest && per - r >= smallest));
+                        longest = std::max(longest, b - a);
+                        for (int64_t q = a; q < b; ++q)
+                            ok &= l.piece_of(q) == w;
+                    }}
+                    if (per <= smallest)
+                        ok &= longest == (int64_t)(tiles + G - 1) / G * per;
+                    if (!ok)
+                        printf("G %d tiles %d smallest %d pieces %d longest %d\\n", G, tiles, smallest, l.pieces, (int)longest);
+                }}""") == []
