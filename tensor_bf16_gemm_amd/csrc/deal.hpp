@@ -57,6 +57,19 @@ struct Line {
     }
 };
 
+// Sums over pieces of K: so many pieces that `workgroups` have about one of
+// `tiles` tiles each, 1 to 16, none shorter than 8 of the `steps` K-steps, and
+// the `plane` bytes of each piece's sums within `room`.
+__host__ __device__ __forceinline__ int sum_pieces(int64_t workgroups, int64_t tiles, int steps, int64_t plane,
+                                                   int64_t room)
+{
+    int64_t n = (workgroups + tiles / 2) / tiles;
+    n = n < steps / 8 ? n : steps / 8;
+    n = n < room / plane ? n : room / plane;
+    n = n < 16 ? n : 16;
+    return n < 1 ? 1 : (int)n;
+}
+
 // Tiles of many rows: unit t of queue x, in hands of `hand` units.
 constexpr int TK_QUEUES = 8;
 __host__ __device__ __forceinline__ int queue_unit(int x, int t, int hand)

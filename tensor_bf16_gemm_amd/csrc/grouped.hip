@@ -162,9 +162,8 @@ void launch_stream_rows(gc::GroupedArgs &a, int blocks, int cus, hipStream_t st)
     }
 }
 
-// Middle sums of the adapters: tiles of 16, 32 or 64 rows, K cut into so many
-// pieces that every CU has about one (tile, piece), but none shorter than 8
-// steps.  (M = 4096, K = 7168, r = 64, 8 adapters: 4 pieces 20 us, 3 pieces
+// Middle sums of the adapters: tiles of 16, 32 or 64 rows, K cut into pieces
+// (sum_pieces).  (M = 4096, K = 7168, r = 64, 8 adapters: 4 pieces 20 us, 3 pieces
 // 24, 7 pieces with smaller rings 27.)
 template <int NB, int RB, int D>
 void launch_sums_rows(gc::GroupedArgs &a, int cus, hipStream_t st)
@@ -173,7 +172,7 @@ void launch_sums_rows(gc::GroupedArgs &a, int cus, hipStream_t st)
     const int64_t most = std::min<int64_t>(a.S, (int64_t)(a.S + bm - 1) / bm + a.E);
     const int64_t about = std::min<int64_t>(a.S, (int64_t)a.S / bm + (RB == 4 ? (a.E + 1) / 2 : a.E));
     a.tiles_n = 1;
-    a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({16, (cus + about / 2) / about, kt / 8}));
+    a.splits = gc::sum_pieces(cus, about, kt, (int64_t)a.S * a.N * 4, kSumBytes);
     const int grid = (int)std::min<int64_t>(most * a.splits, 4 * cus);
     hipLaunchKernelGGL((gc::stream_kernel<NB, RB, D, gc::EPI_SUMS>), dim3(grid), dim3(gc::ST_THREADS), 0, st, a);
 }

@@ -106,3 +106,20 @@ def test_line_is_cut_into_pieces(tmp_path, per_tile):
                     if (!ok)
                         printf("G %d tiles %d smallest %d pieces %d longest %d\\n", G, tiles, smallest, l.pieces, (int)longest);
                 }}""") == []
+
+
+def test_pieces_of_sums_have_room(tmp_path):
+    """However many compute units there are, all pieces' sums fit the workspace (one always does)."""
+    assert run(tmp_path, """
+        const int64_t room = (int64_t)64 << 20;
+        for (int64_t cus : {1, 32, 256, 304, 1024, 4096})
+            for (int64_t S : {1, 17, 64, 1000, 4096, 16384, 131072, 1 << 20})
+                for (int r : {8, 64, 128})
+                    for (int steps : {0, 7, 8, 64, 224, 4096})
+                        for (int bm : {16, 64})
+                            for (int64_t groups : {1, 8, 1000}) {
+                                const int64_t plane = S * r * 4;
+                                const int n = sum_pieces(cus, std::min(S, S / bm + groups), steps, plane, room);
+                                if (n < 1 || n > 16 || (n > 1 && (n * plane > room || steps / n < 8)))
+                                    printf("cus %d S %d r %d steps %d pieces %d\\n", (int)cus, (int)S, r, steps, n);
+                            }""") == []
