@@ -232,7 +232,8 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint8_t *at = ex + (8 * i + (lane >> 3)) * PITCH + (lane & 7) * 32;
-                store16(ro, offset(i, n0), add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]));
+                store16(ro, offset(i, n0),
+                        delta ? add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]) : old[i]);
                 // (past the end: an empty load)
                 old[i] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)offset(i, n0 + EX_COLS), 0, 0);
             }
@@ -380,7 +381,8 @@ __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kerne
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint8_t *at = ex + (4 * i + (lane >> 4)) * PITCH + (lane & 15) * 32;
-                store16(ro, offset(b, i), add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]));
+                store16(ro, offset(b, i),
+                        delta ? add_base(*(const f32x4_t *)at, *(const f32x4_t *)(at + 16), old[i]) : old[i]);
                 old[i] = next[i];
             }
             __builtin_amdgcn_wave_barrier();

@@ -100,3 +100,17 @@ def test_infinite_and_largest_middle_sums(M, G, r):
         # fp32 sums of an adapter with an infinite weight have no bound; their finite ones do
         assert torch.all((got - want).abs()[ok] <= tol[ok])
     assert odd[2, :100].all() and odd[5, :100].all() and ok[6].all()
+
+
+@pytest.mark.parametrize("M,G", [(24, 2), (150, 2)])
+def test_rows_of_no_adapter_are_base_bit_by_bit(M, G):
+    """Every bf16 there is, zeros with a sign and NaN with a payload among them."""
+    g = gen(M)
+    N = (1 << 16) // M // 8 * 8 + 8
+    bits = torch.arange(M * N, dtype=torch.int32) % (1 << 16) - (1 << 15)
+    base = bits.to(torch.int16).view(torch.bfloat16).reshape(M, N)
+    ids = torch.full((M,), -1, dtype=torch.int32)
+    ids[M // 2] = 1
+    got = run(base, randn(g, M, 40), randn(g, G, 40, 16), randn(g, G, 16, N), torch.ones(G), ids).cpu()
+    free = ids < 0
+    assert torch.equal(got[free].view(torch.int16), base[free].view(torch.int16))
