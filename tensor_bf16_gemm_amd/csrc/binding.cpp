@@ -181,6 +181,9 @@ PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         const float *bias = nullptr;
         if (a[3] != Py_None)
             bias = dense(a[3], "bias", at::kFloat, {E}).const_data_ptr<float>();
+        const int renormalize = PyObject_IsTrue(a[4]);
+        if (renormalize < 0)
+            throw Refused{};
         const double scale = PyFloat_AsDouble(a[5]);
         if (scale == -1.0 && PyErr_Occurred())
             throw Refused{};
@@ -192,7 +195,7 @@ PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         Tensor offsets = part(buf, at::kInt, 4 * pairs, {E + 1});
         done(gemm_coll_moe_route(x.const_data_ptr(), type == at::kBFloat16 ? GC_BF16 : GC_F32,
                                  T > 1 ? x.stride(0) : E, T, (int)E, k, small(a[2], "score"), bias,
-                                 PyObject_IsTrue(a[4]), (float)scale, ids.data_ptr<int32_t>(),
+                                 renormalize, (float)scale, ids.data_ptr<int32_t>(),
                                  weights.data_ptr<float>(), offsets.data_ptr<int32_t>(),
                                  rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), address(a[7]),
                                  (uint64_t)whole(a[8]), address(a[6])),

@@ -47,3 +47,13 @@ def test_route_without_workspace(T, E, k, dtype):
     logits = (torch.randn((T, E), generator=gen(T)) * 2).to(dtype)
     check_routing(logits, k, workspace=False)
     check_routing(logits, k, score="sigmoid")
+
+
+def test_renormalize_without_a_truth_value_is_refused():
+    class Neither:
+        def __bool__(self):
+            raise ValueError("neither true nor false")
+    with pytest.raises(ValueError, match="neither"):
+        gc.moe_route(torch.zeros((2, 4), device=DEV), 2, renormalize=Neither())
+    with pytest.raises(TypeError):
+        gc.moe_route(torch.zeros((2, 4), device=DEV), 2, scale="1")
