@@ -70,6 +70,49 @@ __host__ __device__ __forceinline__ int sum_pieces(int64_t workgroups, int64_t t
     return n < 1 ? 1 : (int)n;
 }
 
+// lora_add's second half: its kernel and how much of it a workgroup walks.
+constexpr int EX_THREADS = 256, EX_WAVES = 4, EX_COLS = 64 * EX_WAVES;
+constexpr int XR_COLS = 512, XR_ROWS = 128;              // columns, and most rows, of a workgroup
+
+// Workgroups of expand_kernel that a CU holds at once (their blocks of up fill
+// its LDS), for `steps` steps of 32 that cover r.
+__host__ __device__ constexpr int expand_resident(int steps) { return steps == 1 ? 3 : steps <= 3 ? 2 : 1; }
+
+struct ExpandPlan {
+    bool rows;                 // expand_rows_kernel, else expand_kernel
+    int steps, span, spans;    // see ExpandArgs
+    int64_t grid;
+};
+__host__ __device__ __forceinline__ ExpandPlan expand_plan(int64_t M, int64_t N, int64_t E, int r, int64_t cus)
+{
+    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    ExpandPlan pl = {};
+    pl.steps = (r + 31) / 32;
+    pl.rows = (M + E - 1) / E >= 32;
+    if (pl.rows) {
+        // Rows per workgroup: the fewest (of 16 to 128) with which all
+        // workgroups have a place at once, two per CU (one for r > 64).
+        pl.spans = (int)((N + XR_COLS - 1) / XR_COLS);
+        const int64_t places = cus * (pl.steps <= 2 ? 2 : 1);
+        auto units = [&](int64_t rows) { return least(M, (M + rows - 1) / rows + E) * pl.spans; };
+        pl.span = 16;
+        while (pl.span < XR_ROWS && units(pl.span) > places)
+            pl.span += 16;
+        pl.grid = least(units(pl.span), places);
+        return pl;
+    }
+    // Spans of columns: about as many workgroups as have a place at once.  (The
+    // row tiles counted here are more than there will be.)
+    const int64_t places = cus * expand_resident(pl.steps);
+    const int64_t tiles_n = (N + EX_COLS - 1) / EX_COLS;
+    const int64_t tiles_m = least(M, (M + 15) / 16 + E);
+    const int64_t some = places * 5 / 4 / tiles_m, want = least(tiles_n, some < 1 ? 1 : some);
+    pl.span = (int)((tiles_n + want - 1) / want);
+    pl.spans = (int)((tiles_n + pl.span - 1) / pl.span);
+    pl.grid = least(tiles_m * pl.spans, cus * 8);
+    return pl;
+}
+
 // Tiles of many rows: unit t of queue x, in hands of `hand` units.
 constexpr int TK_QUEUES = 8;
 __host__ __device__ __forceinline__ int queue_unit(int x, int t, int hand)

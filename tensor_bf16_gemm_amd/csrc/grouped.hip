@@ -269,21 +269,12 @@ void launch_tiles(gc::GroupedArgs &a, int splits, int cus, hipStream_t st)
 
 void launch_expand(gc::ExpandArgs &a, int cus, hipStream_t st)
 {
-    const dim3 b(gc::EX_THREADS);
-    const int steps = (a.r + 31) / 32;
-    if ((a.M + a.E - 1) / a.E >= 32) {
-        // Rows per workgroup: the fewest (of 16 to 128) with which all
-        // workgroups have a place at once, two per CU (one for r > 64).
-        a.spans = (a.N + gc::XR_COLS - 1) / gc::XR_COLS;
-        const int64_t places = (int64_t)cus * (steps <= 2 ? 2 : 1);
-        auto units = [&](int rows) {
-            return std::min<int64_t>(a.M, (a.M + rows - 1) / rows + a.E) * a.spans;
-        };
-        a.span = 16;
-        while (a.span < gc::XR_ROWS && units(a.span) > places)
-            a.span += 16;
-        const dim3 g((unsigned)std::min<int64_t>(units(a.span), places));
-        switch (steps) {
+    const gc::ExpandPlan pl = gc::expand_plan(a.M, a.N, a.E, a.r, cus);
+    const dim3 g((unsigned)pl.grid), b(gc::EX_THREADS);
+    a.span = pl.span;
+    a.spans = pl.spans;
+    if (pl.rows) {
+        switch (pl.steps) {
         case 1: hipLaunchKernelGGL((gc::expand_rows_kernel<1>), g, b, 0, st, a); break;
         case 2: hipLaunchKernelGGL((gc::expand_rows_kernel<2>), g, b, 0, st, a); break;
         case 3: hipLaunchKernelGGL((gc::expand_rows_kernel<3>), g, b, 0, st, a); break;
@@ -291,16 +282,7 @@ void launch_expand(gc::ExpandArgs &a, int cus, hipStream_t st)
         }
         return;
     }
-    // Spans of columns: about as many workgroups as have a place at once.  (The
-    // row tiles counted here are more than there will be.)
-    const int64_t places = (int64_t)cus * gc::expand_resident(steps);
-    const int64_t tiles_n = (a.N + gc::EX_COLS - 1) / gc::EX_COLS;
-    const int64_t tiles_m = std::min<int64_t>(a.M, (a.M + 15) / 16 + a.E);
-    const int64_t want = std::min<int64_t>(tiles_n, std::max<int64_t>(1, places * 5 / 4 / tiles_m));
-    a.span = (int)((tiles_n + want - 1) / want);
-    a.spans = (int)((tiles_n + a.span - 1) / a.span);
-    const dim3 g((unsigned)std::min<int64_t>(tiles_m * a.spans, (int64_t)cus * 8));
-    switch (steps) {
+    switch (pl.steps) {
     case 1: hipLaunchKernelGGL((gc::expand_kernel<1>), g, b, 0, st, a); break;
     case 2: hipLaunchKernelGGL((gc::expand_kernel<2>), g, b, 0, st, a); break;
     case 3: hipLaunchKernelGGL((gc::expand_kernel<3>), g, b, 0, st, a); break;

@@ -31,8 +31,6 @@
 
 namespace gc {
 
-constexpr int EX_THREADS = 256, EX_WAVES = 4, EX_COLS = 64 * EX_WAVES;
-
 struct ExpandArgs {
     const uint16_t *base;      // [M][N]
     uint16_t *out;             // [M][N]; base itself or apart from it
@@ -113,9 +111,6 @@ __device__ __forceinline__ f32x4_t whole_product(f32x4_t lead, f32x4_t rest)
         s[i] = s[i] == s[i] ? s[i] : lead[i];
     return s;
 }
-
-// Workgroups that a CU holds at once (their blocks of up fill its LDS).
-constexpr int expand_resident(int steps) { return steps == 1 ? 3 : steps <= 3 ? 2 : 1; }
 
 // KS: steps of 32 that cover r.
 template <int KS>
@@ -244,8 +239,6 @@ __global__ __launch_bounds__(EX_THREADS, expand_resident(KS)) void expand_kernel
         }
     }
 }
-
-constexpr int XR_COLS = 512, XR_ROWS = 128;              // columns, and most rows, of a workgroup
 
 template <int KS>
 __global__ __launch_bounds__(EX_THREADS, KS <= 2 ? 2 : 1) void expand_rows_kernel(ExpandArgs p)

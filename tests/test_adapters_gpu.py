@@ -6,6 +6,7 @@ import torch
 
 import grouped_ref as ref
 import tensor_bf16_gemm_amd as gc
+from adapter_cases import COLUMNS, ROWS
 from gpu_util import log
 
 pytestmark = pytest.mark.gpu
@@ -114,3 +115,27 @@ def test_rows_of_no_adapter_are_base_bit_by_bit(M, G):
     got = run(base, randn(g, M, 40), randn(g, G, 40, 16), randn(g, G, 16, N), torch.ones(G), ids).cpu()
     free = ids < 0
     assert torch.equal(got[free].view(torch.int16), base[free].view(torch.int16))
+
+
+@pytest.mark.parametrize("M,K,N,r,sizes", [c[:5] for c in ROWS + COLUMNS],
+                         ids=lambda v: f"{len(v)}groups" if isinstance(v, list) else str(v))
+def test_walks_of_several_blocks(M, K, N, r, sizes):
+    """Against the 64-bit form, elementwise; apart from base and in its place."""
+    g, G = gen(M + N + r), len(sizes)
+    dg = torch.Generator(DEV)
+    dg.manual_seed(M + N)
+    ids = torch.cat([torch.full((n,), a, dtype=torch.int32) for a, n in enumerate(sizes)]
+                    + [torch.full((M - sum(sizes),), -1, dtype=torch.int32)])
+    ids = ids[torch.randperm(M, generator=g)]
+    X, down = randn(g, M, K).to(DEV), randn(g, G, K, r, scale=K ** -0.5).to(DEV)
+    up = randn(g, G, r, N, scale=r ** -0.5).to(DEV)
+    base = torch.randn((M, N), generator=dg, device=DEV).bfloat16()
+    scale = torch.randn(G, generator=g).to(DEV)
+    log(f"lora M={M} K={K} N={N} r={r} G={G}")
+    want, tol = ref.lora(base, X, down, up, scale, ids.to(DEV))
+    off, rows, _ = gc.group_rows(ids.to(DEV), G)
+    got = gc.lora_add(base, X, down, up, scale, off, rows)
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), torch.nonzero(bad)[0].tolist())
+    same = gc.lora_add(base, X, down, up, scale, off, rows, out=base)
+    assert same is base and torch.equal(same, got)

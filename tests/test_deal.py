@@ -123,3 +123,19 @@ def test_pieces_of_sums_have_room(tmp_path):
                                 if (n < 1 || n > 16 || (n > 1 && (n * plane > room || steps / n < 8)))
                                     printf("cus %d S %d r %d steps %d pieces %d\\n", (int)cus, (int)S, r, steps, n);
                             }""") == []
+
+
+def test_adapter_cases_walk_their_loops(tmp_path):
+    """The sizes of adapter_cases reach what they are there for: the span of rows or columns, and more
+    units of work (with the rows of no adapter, which are copied) than workgroups."""
+    from adapter_cases import COLUMNS, ROWS
+    cases = [(c, True) for c in ROWS] + [(c, False) for c in COLUMNS]
+    out = run(tmp_path, "ExpandPlan p;\n" + "\n".join(
+        f'p = expand_plan({M}, {N}, {len(sizes)}, {r}, 256); printf("%d %d %d %d\\n", p.rows, p.span, p.spans, (int)p.grid);'
+        for (M, K, N, r, sizes, span, again), _ in cases))
+    for ((M, K, N, r, sizes, span, again), many), line in zip(cases, out):
+        rows, got, spans, grid = map(int, line.split())
+        height = got if many else 16
+        units = sum(-(-n // height) for n in [*sizes, M - sum(sizes)]) * spans
+        assert (rows, got, units > grid) == (many, span, again), (M, N, r, line, units)
+        assert sum(sizes) < M

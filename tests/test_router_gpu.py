@@ -57,3 +57,11 @@ def test_renormalize_without_a_truth_value_is_refused():
         gc.moe_route(torch.zeros((2, 4), device=DEV), 2, renormalize=Neither())
     with pytest.raises(TypeError):
         gc.moe_route(torch.zeros((2, 4), device=DEV), 2, scale="1")
+
+
+@pytest.mark.parametrize("T,E,k", [(16500, 24, 2), (17000, 60, 1), (4200, 300, 3), (4100, 600, 2)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_route_blocks_of_several_passes(T, E, k, dtype):
+    """Blocks of more tokens than a workgroup routes at a time (64, or 16 with more than 256 experts)."""
+    logits = (torch.randn((T, E), generator=gen(T)) * 2).to(dtype)
+    check_routing(logits, k, score="sigmoid", scale=2.5)
