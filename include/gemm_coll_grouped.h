@@ -31,6 +31,11 @@
  *   rows     int32 [n]: row of the item at each position (items in no group
  *            come last, after offsets[groups], in their order)
  *   slots    int32 [n]: position of each item, -1 for an item in no group
+ * With the experts first .. first + local - 1 on this rank, the grouping of
+ * ids - first into `local` groups (group_rows) is what the products and the
+ * combine take: the other ranks' pairs get slot -1 and come last.  (The
+ * router's own slots count the pairs of all experts; with a part of its
+ * offsets they would name rows that no product has written.)
  * Groups keep the order of their items.  offsets do not fall.  Kernels read
  * offsets and rows on the device and stay in bounds whatever they hold: an
  * offset is clamped to [0, S], a row outside its matrix reads as zeros (and is
@@ -104,7 +109,9 @@ int gemm_coll_group_rows(const int32_t *ids, int64_t T, int k, int groups, int32
  *   out[i] = bf16(y)                                  GC_ACT_NONE
  *   out[i] = bf16(silu(y[:N/2]) * y[N/2:])            GC_ACT_SILU_GLU
  * with X [T][K], W [E][K][N], rows [S], out [S][N] or [S][N/2].  Positions in
- * no group are left untouched.  N is a multiple of 16 for GC_ACT_SILU_GLU.
+ * no group are left untouched.  The way it runs is chosen for S rows, as if
+ * all were in groups: where most are not, it may be slower than on the rows
+ * that are.  N is a multiple of 16 for GC_ACT_SILU_GLU.
  * With workspace NULL no product is split along K (slower for few rows); the
  * result differs only by the order of fp32 sums, and for given sizes, offsets
  * and device it is the same in every call.
@@ -140,7 +147,8 @@ int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, con
  * Adapters.  For every position i of group a, with m = rows[i],
  *   out[m] = bf16( base[m] + (scale[a] * X[m] . down[a]) . up[a] )
  * with X [M][K], base and out [M][N], down [G][K][r], up [G][r][N],
- * scale float [G], offsets and rows [M] a grouping of the M rows by adapter.
+ * scale float [G], offsets and rows [M] a grouping of all M rows by adapter
+ * (offsets[0] is 0).
  * The middle activations are fp32 sums and are multiplied as such (all 24
  * bits).  Rows in no group: out is base (base == out: untouched).
  * r <= 128, a multiple of 8; G <= 1023.  Needs

@@ -6,13 +6,20 @@ include/gemm_coll_grouped.h.
     y = grouped_gemm(h, w_down, r.offsets)
     out = moe_combine(y, r.slots, r.weights, partials)   # + the other ranks' partial sums
 
+    # with the experts first .. first + local - 1 on this rank: the others' pairs get slot -1
+    g = group_rows(r.ids - first, local)
+    h = grouped_gemm(x, w_up[local ones], g.offsets, g.rows, act="silu_glu")
+    out = moe_combine(grouped_gemm(h, w_down[local ones], g.offsets), g.slots, r.weights, partials)
+
     g = group_rows(adapter_of_row, adapters)
     out = lora_add(out, x, down, up, scale, g.offsets, g.rows, out=out)
 
 Tensors are on the current CUDA (HIP) device; calls are asynchronous on the
 current stream (or ``stream=``, as for the package's other calls).  Each (device, stream) pair gets its own
 workspace, allocated on first use; pass ``workspace=`` (a zero-filled uint8
-tensor) to use one of your own.
+tensor) to use one of your own.  A captured graph keeps the workspace of the
+stream it was captured on: replay it on that stream, or while nothing else
+runs there.
 
 The tensors are checked, the outputs made and the library called in the
 extension module _native (csrc/binding.cpp); these functions add the stream,
