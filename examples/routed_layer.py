@@ -12,8 +12,12 @@ go through
       -> down products                                     (grouped_gemm)
       -> weighted sum + the other ranks' partial sums      (moe_combine)
 
-The other ranks are buffers in this GPU's memory, as everywhere in this
-package.  Prints the time of a pass and the busiest expert.
+The projection is split along K over the ranks: x and the rows of its weights
+are this rank's part, and so are the rows of the adapters' `down`.  Each rank
+adds its own x . down . up to its own product, so the other ranks' partial
+sums of the projection hold their adapters' parts too, and the sum of all is
+the whole X . down . up.  The other ranks are buffers in this GPU's memory, as
+everywhere in this package.  Prints the time of a pass and the busiest expert.
 """
 from __future__ import annotations
 
@@ -33,8 +37,8 @@ import tensor_bf16_gemm_amd as gc  # noqa: E402
 @dataclass
 class Layer:
     """Weights of one rank: projection, adapters, router, experts."""
-    proj: torch.Tensor        # [hidden, hidden]
-    down: torch.Tensor        # [adapters, hidden, rank]
+    proj: torch.Tensor        # [hidden, hidden]: this rank's rows of the projection
+    down: torch.Tensor        # [adapters, hidden, rank]: the same rows of the adapters
     up: torch.Tensor          # [adapters, rank, hidden]
     scale: torch.Tensor       # [adapters]
     router: torch.Tensor      # [hidden, experts]
@@ -56,8 +60,8 @@ def make_layer(hidden: int, inner: int, experts: int, adapters: int, rank: int, 
 
 def forward(p: Layer, x, adapters, proj_peers, moe_peers, k: int, ranks: int):
     """Tokens x [T, hidden]; adapters: gc.group_rows of the tokens' adapters (-1: none); proj_peers
-    and moe_peers [ranks - 1, T, hidden]: the other ranks' partial sums.  Returns the layer's output
-    and the routing."""
+    and moe_peers [ranks - 1, T, hidden]: the other ranks' partial sums (of the projection: with their
+    adapters' parts).  Returns the layer's output and the routing."""
     h = gc.gemm_ar(x, p.proj, proj_peers, R=ranks, rank=0)
     gc.lora_add(h, x, p.down, p.up, p.scale, adapters.offsets, adapters.rows, out=h)
     r = gc.moe_route((h @ p.router).float(), k)
