@@ -379,8 +379,10 @@ __device__ __forceinline__ void route_token(const RouteArgs &p, int t, int j, in
     float val = key_value(Pair::key(mine));
     if (p.bias)
         val = logit<BF16>(p, t, chosen ? id : 0);
-    else if (soft && p.renorm)
-        high = key_value(Pair::key(best));
+    // Renormalized, the chosen terms are relative to the largest of them: with
+    // a bias it may lie so far below the row's maximum that e^(x - high) is 0.
+    if (soft && p.renorm)
+        high = key_value(p.bias ? token_max<LPT>(chosen ? order_key(val) : 0u) : Pair::key(best));
     w = !chosen ? 0.f : soft ? soft_term(val, high) : sigmoid(val);
     if (p.renorm)
         total = token_sum<LPT>(w);

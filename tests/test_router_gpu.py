@@ -65,3 +65,22 @@ def test_route_blocks_of_several_passes(T, E, k, dtype):
     """Blocks of more tokens than a workgroup routes at a time (64, or 16 with more than 256 experts)."""
     logits = (torch.randn((T, E), generator=gen(T)) * 2).to(dtype)
     check_routing(logits, k, score="sigmoid", scale=2.5)
+
+
+@pytest.mark.parametrize("E,k", [(48, 4), (300, 4)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_bias_chooses_experts_far_below_the_maximum(E, k, dtype):
+    """Softmax, renormalized over the chosen: their weights depend on the chosen logits alone, however
+    small their scores are."""
+    g = gen(E)
+    x = torch.randn((9, E), generator=g)
+    x[:, 5] += torch.linspace(0, 400, 9)              # the maximum, which the bias keeps out
+    bias = 2.0 * torch.randperm(E, generator=g).float()
+    bias[5] = -10.0
+    x = x.to(dtype)
+    ids, w = ref.route(x, k, bias=bias)
+    r = gc.moe_route(x.to(DEV), k, bias=bias.to(DEV))
+    log(f"route with bias E={E} {dtype}")
+    assert torch.equal(r.ids.cpu(), ids)
+    # differences of the chosen logits (below 10 here) round by u each, exp and the division by a few
+    assert torch.all((r.weights.cpu().double() - w).abs() <= (10 + 32) * 2 * ref.U * w)
