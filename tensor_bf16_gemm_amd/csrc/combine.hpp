@@ -29,13 +29,8 @@ struct CombineArgs {
     int64_t items;               // T * col_groups
 };
 
-__global__ __launch_bounds__(CB_THREADS) void combine_kernel(CombineArgs p)
+__device__ __forceinline__ void combine_item(const CombineArgs &p, int64_t item, int lane)
 {
-    const int lane = threadIdx.x & 63;
-    const int64_t item =
-        (int64_t)blockIdx.x * CB_WAVES + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    if (item >= p.items)
-        return;
     const int t = (int)(item / p.col_groups);
     const int cg = (int)(item - (int64_t)t * p.col_groups);
     // terms: lane j < k slot j, then the peers
@@ -85,6 +80,16 @@ __global__ __launch_bounds__(CB_THREADS) void combine_kernel(CombineArgs p)
         __builtin_nontemporal_store((u32x4_t){a[0], a[1], b[0], b[1]},
                                     (u32x4_t *)(p.out + (int64_t)t * p.N) + v);
     }
+}
+
+__global__ __launch_bounds__(CB_THREADS) void combine_kernel(CombineArgs p)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t first =
+        (int64_t)blockIdx.x * CB_WAVES + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    // (one item but for more than 2^26 of them)
+    for (int64_t item = first; item < p.items; item += (int64_t)gridDim.x * CB_WAVES)
+        combine_item(p, item, lane);
 }
 
 }  // namespace gc

@@ -478,9 +478,9 @@ int gemm_coll_moe_combine(const gc_bf16 *Y, int64_t S, const int32_t *slots, con
     a.npeers = npeers;
     a.col_groups = (int)((N / 8 + 63) / 64);
     a.items = T * a.col_groups;
-    const int64_t blocks = (a.items + gc::CB_WAVES - 1) / gc::CB_WAVES;
-    if (blocks > INT32_MAX)
-        return GC_ENOTSUP;
+    // (a launch counts its threads in 32 bits)
+    const int64_t blocks =
+        std::min<int64_t>((a.items + gc::CB_WAVES - 1) / gc::CB_WAVES, UINT32_MAX / gc::CB_THREADS);
     hipLaunchKernelGGL(gc::combine_kernel, dim3((unsigned)blocks), dim3(gc::CB_THREADS), 0,
                        (hipStream_t)stream, a);
     return launched();
