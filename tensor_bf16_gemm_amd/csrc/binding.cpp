@@ -49,16 +49,20 @@ const Tensor &tensor(PyObject *o, const char *name)
     return THPVariable_Unpack(o);
 }
 
+// The current device, looked up at the first tensor of a call (-1: not yet).
+thread_local int t_device;
+
 // Refuses a tensor that is not on the current device, whose stream the call
 // is launched on.
 void here(const Tensor &t, const char *name)
 {
     if (!t.is_cuda())
         refuse(PyExc_ValueError, std::string(name) + " must be a device tensor");
-    const auto now = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
-    if (t.device().index() != now)
+    if (t_device < 0)
+        t_device = c10::impl::getDeviceGuardImpl(c10::DeviceType::CUDA)->getDevice().index();
+    if (t.get_device() != t_device)
         refuse(PyExc_ValueError, std::string(name) + " is on " + t.device().str() +
-                                     ", the current device is cuda:" + std::to_string(now));
+                                     ", the current device is cuda:" + std::to_string(t_device));
 }
 
 // A contiguous tensor of the given type on the current device.
@@ -153,6 +157,7 @@ PyObject *guarded(PyObject *const *a, Py_ssize_t n, Py_ssize_t want, F &&f)
         PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", want, n);
         return nullptr;
     }
+    t_device = -1;
     try {
         return f(a);
     } catch (const Refused &) {

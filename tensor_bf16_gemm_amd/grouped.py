@@ -150,7 +150,7 @@ def _place(t, workspace, more: int = 0, stream=None):
 def _on(stream, call, *args):
     """call(*args) for a launch on `stream`.  On a stream that is not the current one the outputs
     come from its memory, and the inputs' is kept until it is through with them."""
-    side = _gc._side(stream)
+    side = None if stream is None else _gc._side(stream)
     if side is None:
         return call(*args)
     with torch.cuda.stream(side):
