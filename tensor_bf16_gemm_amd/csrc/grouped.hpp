@@ -144,6 +144,10 @@ __device__ __forceinline__ int find_group(const int *first, int groups, int t, i
     return base + __builtin_popcountll(b);
 }
 
+// In fp32, with the exponential as 2^(x log2 e) of the hardware: its argument
+// is rounded once, which moves the result by |x| 2^-24 of itself, so by less
+// than 2^-17 where e^-x is finite.  What becomes of it is rounded to bf16
+// (2^-9) at once; expf would take some ten instructions more per value.
 __device__ __forceinline__ float silu(float x) { return x / (1.0f + __expf(-x)); }
 
 __device__ __forceinline__ f32x4_t silu_mul(f32x4_t g, f32x4_t u)
