@@ -197,7 +197,10 @@ struct GroupedPlan {
 
 // The cheapest by three estimates in us, fitted to all of them measured at 391
 // sizes (K 264 to 7168, N 264 to 7168, 1 to 64 groups of 1 to 3900 rows, equal
-// and skewed):
+// and skewed).  Their rates are constants of the fit, with every group that
+// could have a row counted as read, and not the bandwidths that are reached:
+// skewed groups leave some empty (with 48 of 64 groups of K 7168, N 1792 in
+// use, 4.9 TB/s).
 //   stream   reads the weights at 6 TB/s, and again for every further tile of
 //            rows at 11, or at 21 where the L2s hold them; twice as much (half
 //            for PLAIN) where its row pieces are not whole lines of 128 bytes;
@@ -213,11 +216,12 @@ struct GroupedPlan {
 // tile's beginning and end and with the step of a full chip took 1.6 % longer
 // on average, between 0.78 and 1.75 times as long.
 // us measured, stream / tiles / best split: K 7168, N 1792, 64 groups of 16
-// rows with GLU 286 / 276 / 296; 8 groups of 8 rows 37 / 93 / 42, of 64 rows
-// 44 / 101 / 48, of 192 rows 119 / 119 / 75, of 256 rows 154 / 131 / 90, of
-// 1024 rows 453 / 181 / -.  Groups are taken as equally large, as many as there
-// are rows at most; a stream tile has room for twice the average rows, for real
-// groups are not equal.
+// rows with GLU 283 / 276 / 295; 8 groups of 8 rows 37 / 90 / 42, of 64 rows
+// 43 / 96 / 47, of 192 rows 116 / 117 / 70, of 256 rows 153 / 128 / 88 (the
+// choice is three pieces, 94), of 1024 rows 453 / 180 / -.  Groups are taken as
+// equally large, as many as there are rows at most, and all S rows as present;
+// a stream tile has room for twice the average rows, for real groups are not
+// equal.
 GroupedPlan plan_grouped(int64_t S, int64_t K, int64_t N, int64_t F, int E, bool glu, bool workspace, int cus)
 {
     GroupedPlan pl = {};

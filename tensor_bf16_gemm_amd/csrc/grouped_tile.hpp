@@ -21,21 +21,23 @@
 // smallest, so that short tiles come last, and the line of tiles is dealt in
 // hands of two tiles per CU of an XCD to eight queues, one for each, from
 // which its workgroups draw tickets (from the next where theirs is empty).
-// (32768 rows in 64 groups, 4 rounds of tiles: 811 us, against 845 in the
-// order of the groups, and 936 with all short tiles last, which read W twice.)
+// (32768 rows in 64 groups, 4 rounds of tiles: 826 to 860 us by machine; in
+// turn on one machine 811, against 845 in the order of the groups, and 936
+// with all short tiles last, which read W twice.)
 //
 // Fewer tiles than CUs: K is cut into p.splits equal pieces, each unit (piece,
 // tile) leaves its fp32 sums in the workspace, and finish_kernel, a launch of
 // its own at the bandwidth of the whole chip, adds them in the order of K and
-// applies the end.  (8 groups of 256 rows, K 7168, N 1792: 90 us in four
-// pieces, 131 whole.)
+// applies the end.  (8 groups of 256 rows, K 7168, N 1792: 88 us in four
+// pieces, 128 whole.)
 //
 // What bounds it: the fragments' LDS traffic and the power limit, as in
-// gc_kernel (one group of 8192 rows, N 8192, K 7168: 1.38 PFLOP/s, a library
-// product of that size 1.32); with ragged groups also the last round of tiles
+// gc_kernel (one group of 8192 rows, N 8192, K 7168: 1.40 PFLOP/s, a library
+// product of that size 1.36); with ragged groups also the last round of tiles
 // and the rows the tiles are padded with (32768 rows over 64 groups, K 7168,
-// N 1792 with GLU: MFMA busy 52 % of the cycles, CUs busy 84 %), with K = 896
-// the stores (65536 rows, N 7168: 717 of 860 us are left without them).
+// N 1792 with GLU: MFMA busy 53 % of the cycles, CUs busy 83 %), with K = 896
+// the stores (65536 rows, N 7168, 891 us: on a machine where it took 860, 717
+// were left without them).
 #pragma once
 
 #include "grouped.hpp"

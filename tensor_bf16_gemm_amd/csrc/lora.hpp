@@ -21,7 +21,7 @@
 // walk along the columns, every tile of 256 columns waited for its block of
 // up, its base and the last stores in turn: M = 4096, N = 6288, r = 64 took
 // 44 us.)
-// It takes 33 us: 25 at 4.1 TB/s, and 8 before the first row, for the look-up
+// It takes 34 us: 26 at 4.1 TB/s, and 8 before the first row, for the look-up
 // and the sums.
 // expand_kernel, few rows per group: 16 positions, walking along the columns
 // (64 rows of 32 adapters, r = 32: 8 us; one row: 6 us, latencies).
