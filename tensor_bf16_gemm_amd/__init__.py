@@ -9,8 +9,10 @@ HIP kernels.  PyTorch supplies device memory and the stream.
     out = ag_gemm(A, B, shards, flags, status, R=8, rank=3, epoch=1)
 
 The routed and grouped operators of include/gemm_coll_grouped.h (expert
-router, grouped products, combine, adapters) are in .grouped and reached from
-here too.
+router, grouped products, combine, adapters) are in .grouped, those between
+and around the projections of include/gemm_coll_layer.h (RMS norm, e4m3
+quantisation and products, a layer of experts for a few tokens) in .layer;
+both are reached from here too.
 
 Tensors are bf16, contiguous, on the current CUDA (HIP) device.  By default
 each call uses a workspace that lets the kernel split leftover tiles along
@@ -38,7 +40,8 @@ __all__ = ["gemm_ar", "gemm_ar_noalloc", "gemm_rs", "gemm_ar_two_shot", "ag_gemm
            "workspace_bytes", "default_workspace",
            "LIB_PATH", "GC_OK", "GC_EINVAL", "GC_ENOTSUP", "GC_EIO", "GC_ENOSPC",
            "GC_TIMEOUT_BASE",
-           "moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add"]
+           "moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add",
+           "rms_norm", "quantize_fp8", "gemm_fp8", "moe_layer"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libgemm_coll.so")
 
@@ -116,8 +119,9 @@ def lib() -> ctypes.CDLL:
                                      ctypes.c_int, ctypes.c_int, ctypes.c_uint32,
                                      ctypes.POINTER(GcPlan)]
         L.gemm_coll_plan.restype = ctypes.c_int
-        from .grouped_abi import declare
-        declare(L)
+        from . import grouped_abi, layer_abi
+        grouped_abi.declare(L)
+        layer_abi.declare(L)
         _lib = L
     return _lib
 
@@ -454,10 +458,14 @@ _GROUPED = ("moe_route", "group_rows", "grouped_gemm", "moe_combine", "lora_add"
             "grouped_plan", "grouped_workspace_bytes", "lora_workspace_bytes")
 
 
+_LAYER = ("rms_norm", "quantize_fp8", "gemm_fp8", "moe_layer", "Norm", "Quantized", "gemm_fp8_plan")
+
+
 def __getattr__(name):
-    """The routed and grouped operators, from .grouped (which needs torch) on first use."""
-    if name in _GROUPED:
-        from . import grouped
+    """The routed, grouped and layer operators, from .grouped and .layer (which need torch) on first use."""
+    if name in _GROUPED or name in _LAYER:
+        from . import grouped, layer
         globals().update({n: getattr(grouped, n) for n in _GROUPED})
+        globals().update({n: getattr(layer, n) for n in _LAYER})
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

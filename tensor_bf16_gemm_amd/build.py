@@ -3,8 +3,8 @@
 
     python -m tensor_bf16_gemm_amd.build
 
-Compiles csrc/gemm_coll.hip and csrc/grouped.hip (host C ABI + device
-kernels), each in a hipcc of its own, and links them into
+Compiles csrc/gemm_coll.hip, csrc/grouped.hip and csrc/layer.hip (host C ABI +
+device kernels), each in a hipcc of its own, and links them into
 ``tensor_bf16_gemm_amd/libgemm_coll.so``; csrc/binding.cpp (the tensor side of
 the routed and grouped operators, host code against PyTorch's headers) becomes
 ``tensor_bf16_gemm_amd/_native.so``, which finds the library beside itself.
@@ -27,7 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemm_coll.so")
 NATIVE = os.path.join(PKG, "_native.so")
 ARCH = "gfx950"
-SOURCES = ("gemm_coll.hip", "grouped.hip")
+SOURCES = ("gemm_coll.hip", "grouped.hip", "layer.hip")
 
 
 def hipcc() -> str:

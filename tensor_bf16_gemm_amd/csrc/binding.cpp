@@ -1,5 +1,6 @@
-// binding.cpp -- CPython module _native: the tensor side of the routed and
-// grouped operators (checks, outputs, the call into include/gemm_coll_grouped.h).
+// binding.cpp -- CPython module _native: the tensor side of the routed,
+// grouped and layer operators (checks, outputs, the calls into
+// include/gemm_coll_grouped.h and include/gemm_coll_layer.h).
 //
 // A call on a few tokens takes the device 4 to 10 us.  Through ctypes, with
 // the checks and the allocations in Python, the host took 7 to 12 us for it
@@ -13,7 +14,7 @@
 
 #include <string>
 
-#include "gemm_coll_grouped.h"
+#include "gemm_coll_layer.h"
 
 namespace {
 
@@ -39,7 +40,10 @@ std::string text(at::IntArrayRef s)
 
 const char *type_name(at::ScalarType t)
 {
-    return t == at::kBFloat16 ? "torch.bfloat16" : t == at::kFloat ? "torch.float32" : "torch.int32";
+    return t == at::kBFloat16       ? "torch.bfloat16"
+           : t == at::kFloat         ? "torch.float32"
+           : t == at::kFloat8_e4m3fn ? "torch.float8_e4m3fn"
+                                     : "torch.int32";
 }
 
 const Tensor &tensor(PyObject *o, const char *name)
@@ -150,6 +154,81 @@ Tensor part(const Tensor &buf, at::ScalarType type, int64_t byte, at::IntArrayRe
     return t;
 }
 
+// The first `cols` columns of a contiguous matrix, which they keep alive.
+Tensor part_rows(const Tensor &buf, int64_t cols)
+{
+    const int64_t sizes[2] = {buf.size(0), cols}, strides[2] = {buf.size(1), 1};
+    Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(), buf.dtype());
+    t.unsafeGetTensorImpl()->set_sizes_and_strides(at::IntArrayRef(sizes), at::IntArrayRef(strides));
+    return t;
+}
+
+// The other ranks' partials [npeers, rows, cols]: rows contiguous, blocks any
+// distance apart; on another device too, where this one can reach its memory.
+struct Peers {
+    const gc_bf16 *data = nullptr;
+    int n = 0;
+    int64_t stride = 0;
+    Peers(PyObject *o, int64_t rows, int64_t cols)
+    {
+        if (o == Py_None)
+            return;
+        const Tensor &p = tensor(o, "partials");
+        if (p.scalar_type() != at::kBFloat16 || p.dim() != 3 || p.size(1) != rows || p.size(2) != cols)
+            refuse(PyExc_ValueError, "partials: expected bf16 [npeers, " + std::to_string(rows) + ", " +
+                                         std::to_string(cols) + "], got " + c10::toString(p.scalar_type()) +
+                                         " " + text(p.sizes()));
+        if (p.size(0) == 0)
+            return;
+        if (!p.is_cuda())
+            refuse(PyExc_ValueError, "partials must be a device tensor");
+        if (rows * cols > 0 && (p.stride(2) != 1 || (rows > 1 && p.stride(1) != cols)))
+            refuse(PyExc_ValueError, "partials: rows must be contiguous");
+        n = p.size(0) > 16 ? 16 : (int)p.size(0);        // (16 is refused)
+        stride = p.stride(0);
+        data = (const gc_bf16 *)p.const_data_ptr();
+    }
+};
+
+// Logits [T, E] of the router: float32 or bfloat16, rows any distance apart.
+struct Logits {
+    const void *data;
+    int type;
+    int64_t stride, T, E;
+    explicit Logits(PyObject *o)
+    {
+        const Tensor &x = tensor(o, "logits");
+        const at::ScalarType t = x.scalar_type();
+        if (x.dim() != 2 || (t != at::kFloat && t != at::kBFloat16))
+            refuse(PyExc_TypeError, std::string("logits must be float32 or bfloat16 [T, E], got ") +
+                                        c10::toString(t) + " " + text(x.sizes()));
+        here(x, "logits");
+        T = x.size(0);
+        E = x.size(1);
+        if (E > 1 && T > 0 && x.stride(1) != 1)
+            refuse(PyExc_ValueError, "logits: the experts of a row must be contiguous");
+        data = x.const_data_ptr();
+        type = t == at::kBFloat16 ? GC_BF16 : GC_F32;
+        stride = T > 1 ? x.stride(0) : E;
+    }
+};
+
+int truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw Refused{};
+    return v;
+}
+
+double number(PyObject *o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred())
+        throw Refused{};
+    return v;
+}
+
 template <class F>
 PyObject *guarded(PyObject *const *a, Py_ssize_t n, Py_ssize_t want, F &&f)
 {
@@ -171,35 +250,24 @@ PyObject *guarded(PyObject *const *a, Py_ssize_t n, Py_ssize_t want, F &&f)
 PyObject *moe_route(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 {
     return guarded(args, nargs, 9, [](PyObject *const *a) -> PyObject * {
-        const Tensor &x = tensor(a[0], "logits");
-        const at::ScalarType type = x.scalar_type();
-        if (x.dim() != 2 || (type != at::kFloat && type != at::kBFloat16))
-            refuse(PyExc_TypeError, std::string("logits must be float32 or bfloat16 [T, E], got ") +
-                                        c10::toString(type) + " " + text(x.sizes()));
-        here(x, "logits");
-        const int64_t T = x.size(0), E = x.size(1);
+        const Logits logits(a[0]);
+        const Tensor &x = THPVariable_Unpack(a[0]);
+        const int64_t T = logits.T, E = logits.E;
         const int k = small(a[1], "k");
-        if (E > 1 && T > 0 && x.stride(1) != 1)
-            refuse(PyExc_ValueError, "logits: the experts of a row must be contiguous");
         if (k < 1 || E < 1 || E > GC_GROUPS_MAX || k > GC_TOPK_MAX)
             done(GC_EINVAL, "moe_route");
         const float *bias = nullptr;
         if (a[3] != Py_None)
             bias = dense(a[3], "bias", at::kFloat, {E}).const_data_ptr<float>();
-        const int renormalize = PyObject_IsTrue(a[4]);
-        if (renormalize < 0)
-            throw Refused{};
-        const double scale = PyFloat_AsDouble(a[5]);
-        if (scale == -1.0 && PyErr_Occurred())
-            throw Refused{};
+        const int renormalize = truth(a[4]);
+        const double scale = number(a[5]);
         // one allocation for the five outputs, each on a 256-byte boundary
         const int64_t pairs = (T * k * 4 + 255) / 256 * 256;
         const Tensor buf = at::empty({pairs + E / 64 * 64 + 64}, x.options().dtype(at::kInt));
         Tensor ids = part(buf, at::kInt, 0, {T, k}), weights = part(buf, at::kFloat, pairs, {T, k});
         Tensor rows = part(buf, at::kInt, 2 * pairs, {T * k}), slots = part(buf, at::kInt, 3 * pairs, {T, k});
         Tensor offsets = part(buf, at::kInt, 4 * pairs, {E + 1});
-        done(gemm_coll_moe_route(x.const_data_ptr(), type == at::kBFloat16 ? GC_BF16 : GC_F32,
-                                 T > 1 ? x.stride(0) : E, T, (int)E, k, small(a[2], "score"), bias,
+        done(gemm_coll_moe_route(logits.data, logits.type, logits.stride, T, (int)E, k, small(a[2], "score"), bias,
                                  renormalize, (float)scale, ids.data_ptr<int32_t>(),
                                  weights.data_ptr<float>(), offsets.data_ptr<int32_t>(),
                                  rows.data_ptr<int32_t>(), slots.data_ptr<int32_t>(), address(a[7]),
@@ -288,32 +356,14 @@ PyObject *moe_combine(PyObject *, PyObject *const *args, Py_ssize_t nargs)
         const Tensor &slots = dense(a[1], "slots", at::kInt);
         const int64_t S = Y.size(0), N = Y.size(1), T = slots.size(0), k = slots.size(1);
         const Tensor &weights = dense(a[2], "weights", at::kFloat, {T, k});
-        const gc_bf16 *pp = nullptr;
-        int64_t npeers = 0, stride = 0;
-        if (a[3] != Py_None) {
-            const Tensor &p = tensor(a[3], "partials");
-            if (p.scalar_type() != at::kBFloat16 || p.dim() != 3 || p.size(1) != T || p.size(2) != N)
-                refuse(PyExc_ValueError, "partials: expected bf16 [npeers, " + std::to_string(T) + ", " +
-                                             std::to_string(N) + "], got " + c10::toString(p.scalar_type()) +
-                                             " " + text(p.sizes()));
-            if (p.size(0) > 0) {
-                // (on another device too, where this one can reach its memory)
-                if (!p.is_cuda())
-                    refuse(PyExc_ValueError, "partials must be a device tensor");
-                if (T * N > 0 && (p.stride(2) != 1 || (T > 1 && p.stride(1) != N)))
-                    refuse(PyExc_ValueError, "partials: rows must be contiguous");
-                npeers = p.size(0);
-                stride = p.stride(0);
-                pp = (const gc_bf16 *)p.const_data_ptr();
-            }
-        }
+        const Peers peers(a[3], T, N);
         Tensor out = output(a[4], Y, T, N);
-        done(k > GC_TOPK_MAX || npeers > 15
+        done(k > GC_TOPK_MAX
                  ? GC_EINVAL
                  : gemm_coll_moe_combine((const gc_bf16 *)Y.const_data_ptr(), S,
                                          slots.const_data_ptr<int32_t>(), weights.const_data_ptr<float>(), T,
-                                         (int)k, N, pp, (int)npeers, stride, (gc_bf16 *)out.data_ptr(),
-                                         address(a[5])),
+                                         (int)k, N, peers.data, peers.n, peers.stride,
+                                         (gc_bf16 *)out.data_ptr(), address(a[5])),
              "moe_combine");
         return give(a[4], std::move(out));
     });
@@ -351,9 +401,180 @@ PyObject *lora_add(PyObject *, PyObject *const *args, Py_ssize_t nargs)
     });
 }
 
+// Scales [rows, ceil(cols / 128)] by rows: the caller's (float32, the columns
+// contiguous), or new ones whose rows begin on 16 bytes, as gemm_fp8 reads them
+// best.
+Tensor scales_out(PyObject *o, const Tensor &like, int64_t rows, int64_t cols)
+{
+    const int64_t kb = (cols + 127) / 128;
+    if (o == Py_None)
+        return part_rows(at::empty({rows, (kb + 3) / 4 * 4}, like.options().dtype(at::kFloat)), kb);
+    const Tensor &t = tensor(o, "scales");
+    if (t.scalar_type() != at::kFloat || t.dim() != 2 || t.size(0) != rows || t.size(1) != kb)
+        refuse(PyExc_ValueError, "scales: expected float32 [" + std::to_string(rows) + ", " + std::to_string(kb) +
+                                     "], got " + c10::toString(t.scalar_type()) + " " + text(t.sizes()));
+    here(t, "scales");
+    if (rows * kb > 0 && ((kb > 1 && t.stride(1) != 1) || (rows > 1 && t.stride(0) < kb)))
+        refuse(PyExc_ValueError, "scales: the columns must be contiguous and the rows apart");
+    return t;
+}
+
+// (of scales that scales_out has passed)
+int64_t row_stride(const Tensor &t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+
+PyObject *three(PyObject *a, PyObject *b, PyObject *c)
+{
+    PyObject *r = PyTuple_New(3), *all[3] = {a, b, c};
+    if (!r)
+        throw Refused{};
+    for (int i = 0; i < 3; ++i) {
+        if (!all[i]) {
+            Py_INCREF(Py_None);
+            all[i] = Py_None;
+        }
+        PyTuple_SET_ITEM(r, i, all[i]);
+    }
+    return r;
+}
+
+// (x, weight, residual, partials, eps, fp8, out, scales, sum, stream): (y, scales or None, sum or None)
+PyObject *rms_norm(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded(args, nargs, 10, [](PyObject *const *a) -> PyObject * {
+        dims(tensor(a[0], "x"), "x", 2, "[M, N]");
+        const Tensor &x = dense(a[0], "x", at::kBFloat16);
+        const int64_t M = x.size(0), N = x.size(1);
+        const bool wf32 = tensor(a[1], "weight").scalar_type() == at::kFloat;
+        const Tensor &w = dense(a[1], "weight", wf32 ? at::kFloat : at::kBFloat16, {N});
+        const gc_bf16 *residual = nullptr;
+        if (a[2] != Py_None)
+            residual = (const gc_bf16 *)dense(a[2], "residual", at::kBFloat16, {M, N}).const_data_ptr();
+        const Peers peers(a[3], M, N);
+        const double eps = number(a[4]);
+        const bool fp8 = truth(a[5]);
+        const bool summed = residual || peers.n > 0;
+        if (!fp8 && a[7] != Py_None)
+            refuse(PyExc_ValueError, "scales are written with fp8 only");
+        if (!summed && a[8] != Py_None)
+            refuse(PyExc_ValueError, "sum_out without a residual or partials: the sum is x");
+        Tensor y = a[6] != Py_None ? dense(a[6], "out", fp8 ? at::kFloat8_e4m3fn : at::kBFloat16, {M, N})
+                                   : at::empty({M, N}, fp8 ? x.options().dtype(at::kFloat8_e4m3fn) : x.options());
+        Tensor scales, sum;
+        if (fp8)
+            scales = scales_out(a[7], x, M, N);
+        if (summed)
+            sum = a[8] != Py_None ? dense(a[8], "sum_out", at::kBFloat16, {M, N}) : at::empty({M, N}, x.options());
+        done(gemm_coll_rms_norm((const gc_bf16 *)x.const_data_ptr(), residual, peers.data, peers.n, peers.stride,
+                                w.const_data_ptr(), wf32 ? GC_F32 : GC_BF16, (float)eps, M, N,
+                                summed ? (gc_bf16 *)sum.data_ptr() : nullptr,
+                                fp8 ? nullptr : (gc_bf16 *)y.data_ptr(), fp8 ? (gc_e4m3 *)y.data_ptr() : nullptr,
+                                fp8 ? scales.data_ptr<float>() : nullptr, fp8 ? row_stride(scales) : 0,
+                                address(a[9])),
+             "rms_norm");
+        return three(give(a[6], std::move(y)), fp8 ? give(a[7], std::move(scales)) : nullptr,
+                     summed ? give(a[8], std::move(sum)) : nullptr);
+    });
+}
+
+// (x, block_rows, out, scales, stream): (codes, scales)
+PyObject *quantize_fp8(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded(args, nargs, 5, [](PyObject *const *a) -> PyObject * {
+        dims(tensor(a[0], "x"), "x", 2, "[M, K]");
+        const Tensor &x = dense(a[0], "x", at::kBFloat16);
+        const int64_t M = x.size(0), K = x.size(1);
+        const int rows = small(a[1], "block_rows");
+        if (rows != 1 && rows != 128)
+            refuse(PyExc_ValueError, "block_rows must be 1 or 128, got " + std::to_string(rows));
+        Tensor codes = a[2] != Py_None ? dense(a[2], "out", at::kFloat8_e4m3fn, {M, K})
+                                       : at::empty({M, K}, x.options().dtype(at::kFloat8_e4m3fn));
+        const int64_t sr = (M + rows - 1) / rows;
+        Tensor scales = rows == 1        ? scales_out(a[3], x, M, K)
+                        : a[3] != Py_None ? dense(a[3], "scales", at::kFloat, {sr, (K + 127) / 128})
+                                          : at::empty({sr, (K + 127) / 128}, x.options().dtype(at::kFloat));
+        done(gemm_coll_quantize_fp8((const gc_bf16 *)x.const_data_ptr(), M, K, rows, (gc_e4m3 *)codes.data_ptr(),
+                                    scales.data_ptr<float>(), row_stride(scales), address(a[4])),
+             "quantize_fp8");
+        PyObject *r = PyTuple_New(2);
+        if (!r)
+            throw Refused{};
+        PyTuple_SET_ITEM(r, 0, give(a[2], std::move(codes)));
+        PyTuple_SET_ITEM(r, 1, give(a[3], std::move(scales)));
+        return r;
+    });
+}
+
+// (A, a_scales, B, b_scales, partials, out, stream, workspace, bytes)
+PyObject *gemm_fp8(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded(args, nargs, 9, [](PyObject *const *a) -> PyObject * {
+        dims(tensor(a[0], "A"), "A", 2, "[M, K]");
+        dims(tensor(a[2], "B"), "B", 2, "[N, K]");
+        const Tensor &A = dense(a[0], "A", at::kFloat8_e4m3fn);
+        const int64_t M = A.size(0), K = A.size(1), N = tensor(a[2], "B").size(0), kb = (K + 127) / 128;
+        const Tensor &B = dense(a[2], "B", at::kFloat8_e4m3fn, {N, K});
+        const Tensor &sa = tensor(a[1], "a_scales");
+        if (sa.scalar_type() != at::kFloat || sa.dim() != 2 || sa.size(0) != M || sa.size(1) != kb)
+            refuse(PyExc_ValueError, "a_scales: expected float32 [" + std::to_string(M) + ", " + std::to_string(kb) +
+                                         "], got " + c10::toString(sa.scalar_type()) + " " + text(sa.sizes()));
+        here(sa, "a_scales");
+        const Tensor &sb = dense(a[3], "b_scales", at::kFloat, {(N + 127) / 128, kb});
+        const Peers peers(a[4], M, N);
+        Tensor out = a[5] != Py_None ? dense(a[5], "out", at::kBFloat16, {M, N})
+                                     : at::empty({M, N}, A.options().dtype(at::kBFloat16));
+        done(gemm_coll_gemm_fp8((const gc_e4m3 *)A.const_data_ptr(), sa.const_data_ptr<float>(),
+                                M > 1 ? sa.stride(0) : 0, kb > 1 ? sa.stride(1) : 0,
+                                (const gc_e4m3 *)B.const_data_ptr(), sb.const_data_ptr<float>(), M, N, K, peers.data,
+                                peers.n, peers.stride, (gc_bf16 *)out.data_ptr(), address(a[7]),
+                                (uint64_t)whole(a[8]), address(a[6])),
+             "gemm_fp8");
+        return give(a[5], std::move(out));
+    });
+}
+
+// (X, logits, W1, W2, k, score, bias, renormalize, scale, first, partials, out, stream, workspace, bytes)
+PyObject *moe_layer(PyObject *, PyObject *const *args, Py_ssize_t nargs)
+{
+    return guarded(args, nargs, 15, [](PyObject *const *a) -> PyObject * {
+        dims(tensor(a[0], "x"), "x", 2, "[T, K]");
+        dims(tensor(a[2], "w1"), "w1", 3, "[local, K, 2 F]");
+        dims(tensor(a[3], "w2"), "w2", 3, "[local, F, N]");
+        const Tensor &X = dense(a[0], "x", at::kBFloat16);
+        const int64_t T = X.size(0), K = X.size(1);
+        const Logits logits(a[1]);
+        if (logits.T != T)
+            refuse(PyExc_ValueError, "logits has " + std::to_string(logits.T) + " rows, x " + std::to_string(T));
+        const int64_t local = tensor(a[2], "w1").size(0), F2 = tensor(a[2], "w1").size(2);
+        const int64_t N = tensor(a[3], "w2").size(2);
+        const Tensor &W1 = dense(a[2], "w1", at::kBFloat16, {local, K, F2});
+        if (F2 % 2 != 0)
+            refuse(PyExc_ValueError, "w1 has " + std::to_string(F2) + " columns: gate and up are halves");
+        const Tensor &W2 = dense(a[3], "w2", at::kBFloat16, {local, F2 / 2, N});
+        const int k = small(a[4], "k"), first = small(a[9], "first");
+        const float *bias = nullptr;
+        if (a[6] != Py_None)
+            bias = dense(a[6], "bias", at::kFloat, {logits.E}).const_data_ptr<float>();
+        const int renormalize = truth(a[7]);
+        const double scale = number(a[8]);
+        const Peers peers(a[10], T, N);
+        Tensor out = output(a[11], X, T, N);
+        done(logits.E > GC_GROUPS_MAX || local > GC_GROUPS_MAX
+                 ? GC_EINVAL
+                 : gemm_coll_moe_layer((const gc_bf16 *)X.const_data_ptr(), logits.data, logits.type, logits.stride, T,
+                                       (int)logits.E, k, small(a[5], "score"), bias, renormalize, (float)scale,
+                                       (const gc_bf16 *)W1.const_data_ptr(), (const gc_bf16 *)W2.const_data_ptr(),
+                                       first, (int)local, K, F2 / 2, N, peers.data, peers.n, peers.stride,
+                                       (gc_bf16 *)out.data_ptr(), address(a[13]), (uint64_t)whole(a[14]),
+                                       address(a[12])),
+             "moe_layer");
+        return give(a[11], std::move(out));
+    });
+}
+
 #define FAST(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(moe_route), FAST(group_rows), FAST(grouped_gemm), FAST(moe_combine),
-                         FAST(lora_add), {nullptr, nullptr, 0, nullptr}};
+                         FAST(lora_add), FAST(rms_norm), FAST(quantize_fp8), FAST(gemm_fp8), FAST(moe_layer),
+                         {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr,
                           nullptr, nullptr};

@@ -157,7 +157,8 @@ def _on(stream, call, *args):
         r = call(*args)
     here = torch.cuda.current_stream()
     for t in r if isinstance(r, tuple) else (r,):
-        t.record_stream(here)
+        if t is not None:
+            t.record_stream(here)
     _gc._hold(stream, *(t for t in args if isinstance(t, torch.Tensor)))
     return r
 
