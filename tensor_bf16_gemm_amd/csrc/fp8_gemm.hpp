@@ -21,6 +21,8 @@
 // row's 128, so that the lanes of a load together read whole 64-byte pieces.
 #pragma once
 
+#include <utility>
+
 #include "gc_kernel.hpp"
 
 namespace gc {
@@ -44,13 +46,32 @@ struct Fp8Args {
     int splits, piece;         // pieces of K, blocks in each (the last may have fewer)
 };
 
-// 4 bytes global -> LDS at lds + 4 * lane (see dma16).
-__device__ __forceinline__ void dma4(u32x4_t r, uint32_t lds, uint32_t off)
+// 16 or 4 bytes a lane global -> LDS at lds + at, as dma16 does, with a constant
+// part of the LDS address: one scalar instruction for M0.
+template <int AT>
+__device__ __forceinline__ void dma16_at(u32x4_t r, uint32_t lds, uint32_t off)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+    asm volatile("s_add_i32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(lds), "v"(off), "s"(r)
-                 : "memory");
+                 : "s"(lds), "v"(off), "s"(r), "n"(AT)
+                 : "memory", "scc");
+}
+template <int AT>
+__device__ __forceinline__ void dma4_at(u32x4_t r, uint32_t lds, uint32_t off)
+{
+    asm volatile("s_add_i32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(r), "n"(AT)
+                 : "memory", "scc");
+}
+
+// The buffer `by` bytes further on; without a byte if not `on`.
+__device__ __forceinline__ void advance(u32x4_t &r, uint32_t by, bool on)
+{
+    const uint64_t a = (((uint64_t)r[1] << 32) | r[0]) + by;
+    r[0] = (uint32_t)a;
+    r[1] = (uint32_t)(a >> 32);
+    r[2] = on ? r[2] - by : 0u;
 }
 
 __device__ __forceinline__ f32x4_t mfma_e4m3(i32x8_t a, i32x8_t b)
@@ -214,19 +235,65 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 // ---- many rows: tiles through LDS ----
 //
 // Eight waves, 2 along rows and 4 along columns, each 16 * FMT rows by 64
-// columns of a tile of 32 * FMT by 256.  One block of K per step, two stages:
-// the loads of a step are under way while the step before is multiplied.  A row
-// of a stage is 128 bytes, its 16-byte chunk c kept at c ^ (row / 2 % 8), which
-// spreads the 16 lanes of a fragment read's pass over all 64 banks.
+// columns of a tile of 32 * FMT by 256; one block of K per step, two stages in
+// LDS.  A row of a stage is 128 bytes, its 16-byte chunk c kept at c ^ (row / 2
+// % 8), which spreads the 16 lanes of a fragment read's pass over all 64 banks.
+//
+// The two waves of a SIMD both multiply all the time: a wave alone, whose
+// multiply-adds wait for its own matrix instructions, reaches half the rate (in
+// strict turns, one reading while the other multiplied, 8192 x 8192 x 7168 took
+// 555 us).  Fragments are read one group of row blocks ahead, those of B for
+// the next step as its last group frees their registers, and loads are asked
+// for between matrix instructions.
+//
+// Two barriers a step, X at its start and Y in its middle, order the stages.
+// Reads of step b: B and the lower rows of A (lo) after Y of step b - 1, the
+// upper rows (hi) after X of step b.  So hi of step b + 1 is asked for after X
+// and must have landed at the next X; lo, B and the scales of step b + 2 after Y,
+// to have landed at the next Y: each has a whole step.  What a wave has read it
+// has used before it passes the barrier that lets the place be filled again.
 constexpr int F8_THREADS = 512, F8_BN = 256;
-constexpr int F8_A = 256 * 128, F8_B = 256 * 128, F8_SCALES = 8 * 256;
-constexpr int F8_STAGE = F8_A + F8_B + F8_SCALES;
+constexpr int F8_A = 256 * 128, F8_B = 256 * 128, F8_SCALES = 5 * 256;
+constexpr int F8_STAGE = F8_A + F8_B + F8_SCALES, F8_SLOT = 2048;
 
-template <int FMT, bool SUMS>
+// Waits until at most n loads are under way, n one of two constants.
+template <int A, int B>
+__device__ __forceinline__ void wait_either(bool a)
+{
+    if (A == B || a)
+        wait_vmcnt<A>();
+    else
+        wait_vmcnt<B>();
+}
+
+// f(0), f(1), .., f(N - 1), each index a compile-time constant.
+template <class F, int... I>
+__device__ __forceinline__ void each_of(F &f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void each(F &f)
+{
+    each_of(f, std::make_integer_sequence<int, N>{});
+}
+
+// What becomes of a tile: out (with the peers in it), or a piece's sums.
+enum Fp8End { F8_PLAIN = 0, F8_PEERS = 1, F8_SUMS = 2 };
+
+template <int FMT, int END>
 __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 {
-    constexpr int BMt = 32 * FMT, A_LOADS = (FMT + 1) / 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * F8_STAGE];
+    constexpr int BMt = 32 * FMT;
+    constexpr int G = FMT >= 4 ? 2 : 1;                  // row blocks of a group
+    constexpr int GROUPS = (FMT + G - 1) / G, LOG = GROUPS / 2;
+    constexpr int LOR = G * LOG, HIR = FMT - LOR;        // row blocks of a wave in lo, in hi
+    static_assert(GROUPS % 2 == 0, "the first group of a step is fa[0]");
+    // Load instructions of a wave, 8 rows each, for lo and hi of A: waves to a half
+    // of the tile's rows (its two rows of waves), and instructions of a wave.
+    constexpr int LO_W = LOR > 2 ? 8 : 2 * LOR, HI_W = HIR > 2 ? 8 : 2 * HIR;
+    constexpr int LO_N = LO_W == 8 ? 2 : 1, HI_N = HI_W == 8 ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * F8_STAGE + (END == F8_PEERS ? 8 * F8_SLOT : 0)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3, fi = lane & 15, fg = lane >> 4;
@@ -239,49 +306,96 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     const int nt = rest / high, mt = 4 * band + rest - nt * high;
     const int m0 = mt * BMt, n0 = nt * F8_BN;
     const int b0 = pc * p.piece, b1 = min(b0 + p.piece, p.blocks);
-    const u32x4_t rA = make_rsrc4(p.A, (uint32_t)p.M * (uint32_t)p.K);
-    const u32x4_t rB = make_rsrc4(p.B, (uint32_t)p.N * (uint32_t)p.K);
     const uint32_t lds0 = lds_addr(stages);
 
-    // Instruction i of a wave fills rows 8 * (wave + 8 i) .. + 7 of a stage.
+    // A load instruction fills 8 rows of a stage: B's rows 8 (wave + 8 i), A's rows
+    // 8 (wave % W) of the half wave / W (of half i, with all 8 waves in each).
     const int row8 = lane >> 3;
-    uint32_t a_off[A_LOADS], b_off[4];
-    int chunk = (lane & 7) ^ ((row8 >> 1) | ((wave & 1) << 2));
+    const int chunk = (lane & 7) ^ ((row8 >> 1) | ((wave & 1) << 2));
+    const int lo_row = 16 * FMT * (wave / LO_W) + 8 * (wave % LO_W);
+    const int hi_row = 16 * FMT * (wave / HI_W) + 8 * (wave % HI_W) + 16 * LOR;
+    const bool lo_on = wave < 2 * LO_W && wave % LO_W < 2 * LOR, hi_on = wave < 2 * HI_W && wave % HI_W < 2 * HIR;
+    uint32_t lo_off[LO_N], hi_off[HI_N], b_off[4];
+    auto a_offset = [&](int r) {
+        const int m = m0 + r + row8;
+        return m < p.M ? (uint32_t)m * (uint32_t)p.K + 16u * chunk : OOB;
+    };
 #pragma unroll
-    for (int i = 0; i < A_LOADS; ++i) {
-        const int r = 8 * (wave + 8 * i) + row8, m = m0 + r;
-        a_off[i] = r < BMt && m < p.M ? (uint32_t)m * (uint32_t)p.K + 16u * chunk : OOB;
-    }
+    for (int i = 0; i < LO_N; ++i)
+        lo_off[i] = a_offset(lo_row + 16 * FMT * i);
+#pragma unroll
+    for (int i = 0; i < HI_N; ++i)
+        hi_off[i] = a_offset(hi_row + 16 * FMT * i);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = n0 + 8 * (wave + 8 * i) + row8;
         b_off[i] = n < p.N ? (uint32_t)n * (uint32_t)p.K + 16u * chunk : OOB;
     }
-    // Scales: waves 0 to 3 those of 64 rows each, wave 4 those of B's two blocks.
-    u32x4_t rS = make_rsrc4(p.sa, p.sa_bytes);
-    uint32_t s_off = OOB, s_step = p.sa_block;
-    if (wave < 4) {
-        const int m = m0 + 64 * wave + lane;
-        if (m < p.M)
-            s_off = (uint32_t)m * p.sa_row;
-    } else if (wave == 4) {
-        rS = make_rsrc4(p.sb, (uint32_t)((p.N + 127) / 128) * (uint32_t)p.blocks * 4u);
-        s_step = 4;
-        const int nb = 2 * nt + lane;
-        if (lane < 2 && 128 * nb < p.N)
-            s_off = (uint32_t)nb * (uint32_t)p.blocks * 4u;
-    }
-    auto load = [&](int b, uint32_t st) {
-        const bool on = b < b1 && 128 * b + 16 * chunk < p.K;
-        const uint32_t k0 = 128u * (uint32_t)b;
+    // Scales: waves 0 to 3 those of 64 rows each, the others those of B's two blocks.
+    const bool of_b = wave >= 4;
+    const uint32_t s_step = of_b ? 4u : p.sa_block;
+    const int s_at = of_b ? 2 * nt + lane : m0 + 64 * wave + lane;
+    const uint32_t s_off = (of_b ? lane < 2 && 128 * s_at < p.N : s_at < p.M)
+                               ? (uint32_t)s_at * (of_b ? (uint32_t)p.blocks * 4u : p.sa_row)
+                               : OOB;
+    // Buffers that begin at the block to be loaded next (and hold nothing past the
+    // piece), so that a lane's offsets stay as they are: B, lo and the scales run
+    // ahead of hi.  The chunks past K of the last block are masked.
+    u32x4_t rB = make_rsrc4(p.B, (uint32_t)p.N * (uint32_t)p.K);
+    u32x4_t rLo = make_rsrc4(p.A, (uint32_t)p.M * (uint32_t)p.K);
+    u32x4_t rS = make_rsrc4((const void *)(of_b ? (uint64_t)p.sb : (uint64_t)p.sa),
+                            of_b ? (uint32_t)((p.N + 127) / 128) * (uint32_t)p.blocks * 4u : p.sa_bytes);
+    const bool first_on = b0 < b1;
+    advance(rB, 128u * (uint32_t)b0, first_on);
+    advance(rLo, 128u * (uint32_t)b0, first_on);
+    advance(rS, s_step * (uint32_t)b0, first_on);
+    u32x4_t rHi = rLo;
+    const bool ragged = p.K % 128 != 0;
+    const int tail_off = p.K - 128 * (p.blocks - 1);      // bytes of the last block
+    // After X, hi; after Y: instruction i of B, lo and scales.  `to`: the stage's
+    // address and the wave's place in it.
+    constexpr int Y_N = 4 + LO_N + 1;
+    auto load_x = [&](uint32_t st, auto c) {
+        constexpr int i = decltype(c)::value;
+        if (hi_on)
+            dma16_at<i * 16 * FMT * 128>(rHi, st + (uint32_t)(hi_row * 128), hi_off[i]);
+    };
+    auto load_y = [&](uint32_t st, auto c) {
+        constexpr int i = decltype(c)::value;
+        if constexpr (i < 4)
+            dma16_at<F8_A + i * 8192>(rB, st + (uint32_t)(wave * 1024), b_off[i]);
+        else if constexpr (i < 4 + LO_N) {
+            if (lo_on)
+                dma16_at<(i - 4) * 16 * FMT * 128>(rLo, st + (uint32_t)(lo_row * 128), lo_off[i - 4]);
+        } else
+            dma4_at<F8_A + F8_B>(rS, st + (uint32_t)(min(wave, 4) * 256), s_off);
+    };
+    auto mask_x = [&](int b) {
+        if (ragged && b == p.blocks - 1 && 16 * chunk >= tail_off) {
 #pragma unroll
-        for (int i = 0; i < A_LOADS; ++i)
-            if (8 * i + wave < 4 * FMT)
-                dma16(rA, st + (uint32_t)((wave + 8 * i) * 1024), on ? a_off[i] + k0 : OOB);
+            for (int i = 0; i < HI_N; ++i)
+                hi_off[i] = OOB;
+        }
+    };
+    auto mask_y = [&](int b) {
+        if (ragged && b == p.blocks - 1 && 16 * chunk >= tail_off) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dma16(rB, st + (uint32_t)(F8_A + (wave + 8 * i) * 1024), on ? b_off[i] + k0 : OOB);
-        dma4(rS, st + (uint32_t)(F8_A + F8_B + wave * 256), b < b1 ? s_off + s_step * (uint32_t)b : OOB);
+            for (int i = 0; i < 4; ++i)
+                b_off[i] = OOB;
+#pragma unroll
+            for (int i = 0; i < LO_N; ++i)
+                lo_off[i] = OOB;
+        }
+    };
+    auto next_x = [&](int b) {                           // hi goes on to block b
+        advance(rHi, 128u, b < b1);
+        mask_x(b);
+    };
+    auto next_y = [&](int b) {                           // the others
+        advance(rB, 128u, b < b1);
+        advance(rLo, 128u, b < b1);
+        advance(rS, s_step, b < b1);
+        mask_y(b);
     };
     const uint32_t key = (uint32_t)((fi >> 1) & 7);
     const uint32_t frag = (uint32_t)(fi * 128) + ((fg ^ key) << 4);
@@ -296,31 +410,216 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-    auto fragment = [&](uint32_t at) { return join(*lds_ptr<u32x4_t>(at), *lds_ptr<u32x4_t>(at ^ 64)); };
-    load(b0, lds0);
-    int cur = 0;
+    // Row block i of an operand whose fragments begin at lo and, 64 bytes apart, hi.
+    auto fragment = [&](uint32_t lo, uint32_t hi, int i) {
+        return join(*lds_ptr<u32x4_t>(lo + (uint32_t)(i * 2048)), *lds_ptr<u32x4_t>(hi + (uint32_t)(i * 2048)));
+    };
+
+    // The peers: item w of a wave is its block of 16 rows w % FMT and 64 columns
+    // of peer w / FMT, 2 KiB that are asked for at the end of one step, into a
+    // place of the wave's own in LDS, and added after Y of the next.  (16-byte
+    // chunk c of row r is kept at c ^ (r / 2 % 8), as in a stage.)
+    const int items = END == F8_PEERS ? FMT * p.npeers : 0;
+    const uint32_t slot = lds0 + (uint32_t)(2 * F8_STAGE + wave * F8_SLOT);
+    const uint32_t p_slot = (uint32_t)(fi * 128 + (((fg >> 1) ^ ((fi >> 1) & 7)) << 4) + 8 * (fg & 1));
+    // Buffer that begins at item w: what is read past a row's end is not stored,
+    // past the peer's last row it is 0.
+    auto peer_at = [&](int w, const uint16_t *&from) {
+        const int q = w / FMT;
+        const int64_t at = (int64_t)(m0 + 16 * (wm * FMT + w - q * FMT)) * p.N + n0 + 64 * wn;
+        const int64_t left = (int64_t)p.M * p.N - at;
+        from = p.partials + q * p.peer_stride + at;
+        return left > 0 ? (uint32_t)left * 2u : 0u;
+    };
+    auto ask = [&](int w) {
+        const uint16_t *from;
+        const uint32_t bytes = peer_at(w, from);
+        const u32x4_t r = make_rsrc4(from, bytes);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+            dma16_nt(r, slot + (uint32_t)(i * 1024), (uint32_t)row * (uint32_t)p.N * 2u + 16u * c);
+        }
+    };
+    // (The empty asm statements differ, so that the cases stay apart: as one, they
+    // would index the accumulators, which then were no registers.)
+    auto add_to = [&](auto c) {
+        constexpr int i = decltype(c)::value;
+        if constexpr (i < FMT) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                acc[i][j] += unpack_bf16x4(*lds_ptr<u32x2_t>(slot + (p_slot ^ (uint32_t)(32 * j))));
+                if (j == 1)
+                    __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        asm volatile("; %0" : : "n"(i));
+    };
+    auto add_item = [&](int w) {
+        switch (w % FMT) {
+        case 0: add_to(std::integral_constant<int, 0>{}); break;
+        case 1: add_to(std::integral_constant<int, 1>{}); break;
+        case 2: add_to(std::integral_constant<int, 2>{}); break;
+        case 3: add_to(std::integral_constant<int, 3>{}); break;
+        case 4: add_to(std::integral_constant<int, 4>{}); break;
+        case 5: add_to(std::integral_constant<int, 5>{}); break;
+        case 6: add_to(std::integral_constant<int, 6>{}); break;
+        default: add_to(std::integral_constant<int, 7>{}); break;
+        }
+    };
+
+    auto all_y = [&](uint32_t st) {
+        load_y(st, std::integral_constant<int, 0>{});
+        load_y(st, std::integral_constant<int, 1>{});
+        load_y(st, std::integral_constant<int, 2>{});
+        load_y(st, std::integral_constant<int, 3>{});
+        load_y(st, std::integral_constant<int, 4>{});
+        load_y(st, std::integral_constant<int, 5>{});
+        if constexpr (Y_N > 6)
+            load_y(st, std::integral_constant<int, 6>{});
+    };
+    auto all_x = [&](uint32_t st) {
+        load_x(st, std::integral_constant<int, 0>{});
+        if constexpr (HI_N > 1)
+            load_x(st, std::integral_constant<int, 1>{});
+    };
+    mask_x(b0);
+    mask_y(b0);
+    all_y(lds0);
+    all_x(lds0);
+    next_y(b0 + 1);
+    all_y(lds0 + (uint32_t)F8_STAGE);
+    wait_vmcnt<0>();
+    barrier_only();
+    i32x8_t fb[4], fa[2][G];
+    uint32_t a_lo = lds0 + a_frag, a_hi = lds0 + (a_frag ^ 64);      // in the stage of this step
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        fb[j] = fragment(lds0 + b_frag, lds0 + (b_frag ^ 64), j);
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+        fa[0][i] = fragment(a_lo, a_hi, i);
+    int cur = 0, item = 0;                               // items asked for
     for (int b = b0; b < b1; ++b) {
-        wait_vmcnt<0>();
-        barrier_only();
         const uint32_t st = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
         cur ^= 1;
-        load(b + 1, lds0 + (uint32_t)(cur * F8_STAGE));
-        const float sb = *lds_ptr<float>(st + t_frag);
-        i32x8_t fb[4];
+        const uint32_t other = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
+        next_x(b + 1);
+        next_y(b + 2);
+        // X: hi of this step has landed
+        if (END == F8_PEERS && b > b0 && b - b0 <= items)          // (and an item is under way)
+            wait_either<Y_N + 2, Y_N - LO_N + 2>(lo_on);
+        else
+            wait_either<Y_N, Y_N - LO_N>(lo_on);
+        barrier_only();
+        float s[FMT];
+        {
+            const float sb = *lds_ptr<float>(st + t_frag);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            fb[j] = fragment(st + b_frag + j * 2048);
-#pragma unroll
-        for (int i = 0; i < FMT; ++i) {
-            const i32x8_t fa = fragment(st + a_frag + i * 2048);
-            const float s = *lds_ptr<float>(st + s_frag + i * 64) * sb;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[i][j] += mfma_e4m3(fb[j], fa) * s;
+            for (int i = 0; i < FMT; ++i)
+                s[i] = *lds_ptr<float>(st + s_frag + i * 64) * sb;
         }
-        wait_lgkmcnt0();
+        constexpr int TRAIL = 3, COUNT = 4 * FMT;
+        f32x4_t r[TRAIL + 1];
+        uint32_t an_lo, an_hi, bn_lo, bn_hi;             // in the next step's stage
+        // Matrix instruction n of the step: group n / (4 G), in it column block by
+        // column block.
+        auto row_of = [](int n) {
+            const int g = n / (4 * G), high_g = FMT - g * G < G ? FMT - g * G : G;
+            return g * G + (n - g * 4 * G) % high_g;
+        };
+        auto col_of = [](int n) {
+            const int g = n / (4 * G), high_g = FMT - g * G < G ? FMT - g * G : G;
+            return (n - g * 4 * G) / high_g;
+        };
+        auto turn = [&](auto c) {
+            constexpr int n = decltype(c)::value, g = n / (4 * G), in = n - g * 4 * G;
+            constexpr int EVERY = COUNT - 4 * LOR >= 2 * Y_N ? 2 : 1;
+            if constexpr (n == 4 * LOR) {
+                // Y: B, lo and the scales of the next step have landed, the peers' item
+                // too; this step's scales have been read
+#pragma unroll
+                for (int i = 0; i < FMT; ++i)
+                    asm volatile("" : : "v"(s[i]));
+                wait_either<HI_N, 0>(hi_on);
+                barrier_only();
+            }
+            if constexpr (n < COUNT && in == 0) {
+                // the next group's rows
+                if (g == GROUPS - 1) {
+                    an_lo = other + a_frag;
+                    an_hi = other + (a_frag ^ 64);
+                    bn_lo = other + b_frag;
+                    bn_hi = other + (b_frag ^ 64);
+                }
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    if (g == GROUPS - 1)
+                        fa[0][i] = fragment(an_lo, an_hi, i);
+                    else if ((g + 1) * G + i < FMT)
+                        fa[(g + 1) % 2][i] = fragment(a_lo, a_hi, (g + 1) * G + i);
+                }
+            }
+            if constexpr (n < COUNT)
+                r[n % (TRAIL + 1)] = mfma_e4m3(fb[col_of(n)], fa[g % 2][row_of(n) - g * G]);
+            if constexpr (n >= TRAIL) {
+                constexpr int o = n - TRAIL;
+                f32x4_t &x = acc[row_of(o)][col_of(o)];
+                x += r[o % (TRAIL + 1)] * s[row_of(o)];
+                asm volatile("" : "+v"(x));              // (here, not where it is needed next)
+            }
+            // the last use of a fragment of B in this step
+            if constexpr (n < COUNT && g == GROUPS - 1 && (n + 1 == COUNT || col_of(n + 1) != col_of(n)))
+                fb[col_of(n)] = fragment(bn_lo, bn_hi, col_of(n));
+            // loads: hi of the next step after X, the rest of the one after it after Y
+            if constexpr (n < 4 * LOR) {
+                if constexpr (n % 2 == 1 && n / 2 < HI_N)
+                    load_x(other, std::integral_constant<int, n / 2>{});
+            } else if constexpr (n < COUNT) {
+                constexpr int k = n - 4 * LOR;
+                if constexpr (k % EVERY == EVERY - 1 && k / EVERY < Y_N)
+                    load_y(st, std::integral_constant<int, k / EVERY>{});
+            } else if constexpr (COUNT - 4 * LOR + n - COUNT < Y_N && EVERY == 1) {
+                load_y(st, std::integral_constant<int, n - 4 * LOR>{});
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        static_assert(COUNT + TRAIL - 4 * LOR >= Y_N, "turns for the loads");
+        each<COUNT + TRAIL>(turn);
+        a_lo = an_lo;
+        a_hi = an_hi;
+        if constexpr (END == F8_PEERS) {
+            if (b > b0 && item > 0 && b - b0 <= items)
+                add_item(item - 1);
+            if (item < items)
+                ask(item++);
+        }
     }
     wait_vmcnt<0>();
+    if constexpr (END == F8_PEERS) {
+        // the item under way, and what the steps of K did not reach, a peer at a time
+        if (item > 0 && b1 - b0 <= items)
+            add_item(item - 1);
+        for (int q = item / FMT; q < p.npeers; ++q) {
+            u32x2_t w[FMT][4];
+#pragma unroll
+            for (int i = 0; i < FMT; ++i) {
+                const uint16_t *from;
+                const uint32_t bytes = peer_at(q * FMT + i, from);
+                const __amdgpu_buffer_rsrc_t rp = make_rsrc(from, q * FMT + i < item ? 0u : bytes);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[i][j] = __builtin_bit_cast(
+                        u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                     rp, (int)(((uint32_t)fi * (uint32_t)p.N + 4u * fg) * 2u + 32u * j), 0, 0));
+            }
+#pragma unroll
+            for (int i = 0; i < FMT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[i][j] += unpack_bf16x4(w[i][j]);
+        }
+    }
 
     const int ln = opaque_v(lane);
     const int fi2 = ln & 15, fg2 = ln >> 4;
@@ -335,12 +634,11 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             if (m >= p.M || n >= p.N)
                 continue;
             const int64_t at = (int64_t)m * p.N + n;
-            if constexpr (SUMS) {
+            if constexpr (END == F8_SUMS) {
                 float *to = p.sums + (size_t)pc * p.M * p.N + at;
                 *(f32x4_t *)to = (f32x4_t){v[0], v[1], v[2], v[3]};
                 *(f32x4_t *)(to + 4) = (f32x4_t){v[4], v[5], v[6], v[7]};
             } else {
-                add_peers(v, p.partials, p.peer_stride, p.npeers, at);
                 *(u32x4_t *)(p.out + at) = pack_bf16x8(v);
             }
         }

@@ -55,10 +55,13 @@ void launch_fp8_tiles(gc::Fp8Args &a, int cus, hipStream_t st)
     a.splits = std::max(1, (a.blocks + a.piece - 1) / a.piece);
     const dim3 grid(a.tiles_m * a.tiles_n * a.splits), b(gc::F8_THREADS);
     if (a.splits == 1) {
-        hipLaunchKernelGGL((gc::fp8_tile_kernel<FMT, false>), grid, b, 0, st, a);
+        if (a.npeers > 0)
+            hipLaunchKernelGGL((gc::fp8_tile_kernel<FMT, gc::F8_PEERS>), grid, b, 0, st, a);
+        else
+            hipLaunchKernelGGL((gc::fp8_tile_kernel<FMT, gc::F8_PLAIN>), grid, b, 0, st, a);
         return;
     }
-    hipLaunchKernelGGL((gc::fp8_tile_kernel<FMT, true>), grid, b, 0, st, a);
+    hipLaunchKernelGGL((gc::fp8_tile_kernel<FMT, gc::F8_SUMS>), grid, b, 0, st, a);
     const int64_t vecs = (int64_t)a.M * a.N / 8;
     const int fin = (int)std::min<int64_t>((vecs + gc::F8_FINISH - 1) / gc::F8_FINISH, 8 * cus);
     hipLaunchKernelGGL(gc::fp8_finish_kernel, dim3(fin), dim3(gc::F8_FINISH), 0, st, a);
