@@ -253,8 +253,8 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 // to have landed at the next Y: each has a whole step.  What a wave has read it
 // has used before it passes the barrier that lets the place be filled again.
 constexpr int F8_THREADS = 512, F8_BN = 256;
-constexpr int F8_A = 256 * 128, F8_B = 256 * 128, F8_SCALES = 5 * 256;
-constexpr int F8_STAGE = F8_A + F8_B + F8_SCALES, F8_SLOT = 2048;
+constexpr int F8_B = 256 * 128, F8_SCALES = 5 * 256;
+constexpr int F8_SLOT = 2048;                            // a wave's place for a block of a peer
 
 // Waits until at most n loads are under way, n one of two constants.
 template <int A, int B>
@@ -284,7 +284,8 @@ enum Fp8End { F8_PLAIN = 0, F8_PEERS = 1, F8_SUMS = 2 };
 template <int FMT, int END>
 __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 {
-    constexpr int BMt = 32 * FMT;
+    constexpr int BMt = 32 * FMT, F8_A = BMt * 128, F8_STAGE = F8_A + F8_B + F8_SCALES;
+    constexpr int SLOTS = FMT == 8 ? 1 : 2;              // (as LDS has room)
     constexpr int G = FMT >= 4 ? 2 : 1;                  // row blocks of a group
     constexpr int GROUPS = (FMT + G - 1) / G, LOG = GROUPS / 2;
     constexpr int LOR = G * LOG, HIR = FMT - LOR;        // row blocks of a wave in lo, in hi
@@ -293,7 +294,7 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     // of the tile's rows (its two rows of waves), and instructions of a wave.
     constexpr int LO_W = LOR > 2 ? 8 : 2 * LOR, HI_W = HIR > 2 ? 8 : 2 * HIR;
     constexpr int LO_N = LO_W == 8 ? 2 : 1, HI_N = HI_W == 8 ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * F8_STAGE + (END == F8_PEERS ? 8 * F8_SLOT : 0)];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * F8_STAGE + (END == F8_PEERS ? 8 * SLOTS * F8_SLOT : 0)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3, fi = lane & 15, fg = lane >> 4;
@@ -416,56 +417,31 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     };
 
     // The peers: item w of a wave is its block of 16 rows w % FMT and 64 columns
-    // of peer w / FMT, 2 KiB that are asked for at the end of one step, into a
-    // place of the wave's own in LDS, and added after Y of the next.  (16-byte
-    // chunk c of row r is kept at c ^ (r / 2 % 8), as in a stage.)
+    // of peer w / FMT, 2 KiB.  It is asked for at the end of step w, into one of
+    // SLOTS places of the wave's own in LDS, and added at the end of step w + SLOTS.
+    // (16-byte chunk c of row r is kept at c ^ (r / 2 % 8), as in a stage.)
     const int items = END == F8_PEERS ? FMT * p.npeers : 0;
-    const uint32_t slot = lds0 + (uint32_t)(2 * F8_STAGE + wave * F8_SLOT);
+    const uint32_t slots = lds0 + (uint32_t)(2 * F8_STAGE + wave * SLOTS * F8_SLOT);
     const uint32_t p_slot = (uint32_t)(fi * 128 + (((fg >> 1) ^ ((fi >> 1) & 7)) << 4) + 8 * (fg & 1));
-    // Buffer that begins at item w: what is read past a row's end is not stored,
-    // past the peer's last row it is 0.
-    auto peer_at = [&](int w, const uint16_t *&from) {
-        const int q = w / FMT;
-        const int64_t at = (int64_t)(m0 + 16 * (wm * FMT + w - q * FMT)) * p.N + n0 + 64 * wn;
-        const int64_t left = (int64_t)p.M * p.N - at;
-        from = p.partials + q * p.peer_stride + at;
-        return left > 0 ? (uint32_t)left * 2u : 0u;
+    // Buffer of row block i of a peer whose part of the wave begins at `part`: what
+    // is read past a row's end is not stored, past the peer's last row it is 0.
+    const int64_t part_at = (int64_t)(m0 + 16 * FMT * wm) * p.N + n0 + 64 * wn;
+    auto peer_bytes = [&](int i) {
+        const int rows = min(p.M - (m0 + 16 * (FMT * wm + i)), 16);
+        return (uint32_t)max(2 * (rows * p.N - (n0 + 64 * wn)), 0);
     };
-    auto ask = [&](int w) {
-        const uint16_t *from;
-        const uint32_t bytes = peer_at(w, from);
-        const u32x4_t r = make_rsrc4(from, bytes);
+    auto ask = [&](const uint16_t *part, int i, uint32_t slot) {
+        const u32x4_t r = make_rsrc4(part + (int64_t)(16 * i) * p.N, peer_bytes(i));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int row = 8 * i + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
-            dma16_nt(r, slot + (uint32_t)(i * 1024), (uint32_t)row * (uint32_t)p.N * 2u + 16u * c);
+        for (int d = 0; d < 2; ++d) {
+            const int row = 8 * d + (lane >> 3), c = (lane & 7) ^ ((row >> 1) & 7);
+            dma16_nt(r, slot + (uint32_t)(d * 1024), (uint32_t)row * (uint32_t)p.N * 2u + 16u * c);
         }
     };
-    // (The empty asm statements differ, so that the cases stay apart: as one, they
-    // would index the accumulators, which then were no registers.)
-    auto add_to = [&](auto c) {
-        constexpr int i = decltype(c)::value;
-        if constexpr (i < FMT) {
+    auto add_item = [&](uint32_t slot, f32x4_t (&x)[4]) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                acc[i][j] += unpack_bf16x4(*lds_ptr<u32x2_t>(slot + (p_slot ^ (uint32_t)(32 * j))));
-                if (j == 1)
-                    __builtin_amdgcn_sched_barrier(0);
-            }
-        }
-        asm volatile("; %0" : : "n"(i));
-    };
-    auto add_item = [&](int w) {
-        switch (w % FMT) {
-        case 0: add_to(std::integral_constant<int, 0>{}); break;
-        case 1: add_to(std::integral_constant<int, 1>{}); break;
-        case 2: add_to(std::integral_constant<int, 2>{}); break;
-        case 3: add_to(std::integral_constant<int, 3>{}); break;
-        case 4: add_to(std::integral_constant<int, 4>{}); break;
-        case 5: add_to(std::integral_constant<int, 5>{}); break;
-        case 6: add_to(std::integral_constant<int, 6>{}); break;
-        default: add_to(std::integral_constant<int, 7>{}); break;
-        }
+        for (int j = 0; j < 4; ++j)
+            x[j] += unpack_bf16x4(*lds_ptr<u32x2_t>(slot + (p_slot ^ (uint32_t)(32 * j))));
     };
 
     auto all_y = [&](uint32_t st) {
@@ -499,15 +475,21 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 #pragma unroll
     for (int i = 0; i < G; ++i)
         fa[0][i] = fragment(a_lo, a_hi, i);
-    int cur = 0, item = 0;                               // items asked for
-    for (int b = b0; b < b1; ++b) {
+    int cur = 0;
+    [[maybe_unused]] const uint16_t *part = p.partials + part_at;    // of the peer that is asked for
+    // Step b, the U-th of FMT (of which each has its own row block of the peers, so
+    // that the accumulators it enters are known).
+    auto run = [&](auto uc, int b) {
+        [[maybe_unused]] constexpr int U = decltype(uc)::value;
         const uint32_t st = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
         cur ^= 1;
         const uint32_t other = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
         next_x(b + 1);
         next_y(b + 2);
         // X: hi of this step has landed
-        if (END == F8_PEERS && b > b0 && b - b0 <= items)          // (and an item is under way)
+        const int step = b - b0;
+        const bool asked = END == F8_PEERS && step > 0 && step <= items;     // an item, at the end of the step before
+        if (asked)
             wait_either<Y_N + 2, Y_N - LO_N + 2>(lo_on);
         else
             wait_either<Y_N, Y_N - LO_N>(lo_on);
@@ -536,12 +518,15 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             constexpr int n = decltype(c)::value, g = n / (4 * G), in = n - g * 4 * G;
             constexpr int EVERY = COUNT - 4 * LOR >= 2 * Y_N ? 2 : 1;
             if constexpr (n == 4 * LOR) {
-                // Y: B, lo and the scales of the next step have landed, the peers' item
-                // too; this step's scales have been read
+                // Y: B, lo and the scales of the next step have landed, and the item
+                // asked for before them; this step's scales have been read
 #pragma unroll
                 for (int i = 0; i < FMT; ++i)
                     asm volatile("" : : "v"(s[i]));
-                wait_either<HI_N, 0>(hi_on);
+                if (asked && SLOTS == 2)
+                    wait_either<HI_N + 2, 2>(hi_on);
+                else
+                    wait_either<HI_N, 0>(hi_on);
                 barrier_only();
             }
             if constexpr (n < COUNT && in == 0) {
@@ -589,24 +574,48 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
         a_lo = an_lo;
         a_hi = an_hi;
         if constexpr (END == F8_PEERS) {
-            if (b > b0 && item > 0 && b - b0 <= items)
-                add_item(item - 1);
-            if (item < items)
-                ask(item++);
+            const uint32_t slot = slots + (uint32_t)((step & (SLOTS - 1)) * F8_SLOT);
+            if (step >= SLOTS && step - SLOTS < items)
+                add_item(slot, acc[(U + FMT - SLOTS % FMT) % FMT]);
+            if (step < items)
+                ask(part, U, slot);
+            if (U == FMT - 1)
+                part += p.peer_stride;
         }
+    };
+    if constexpr (END == F8_PEERS) {
+        int b = b0;
+        auto in_turn = [&](auto uc) {
+            if (b < b1)
+                run(uc, b++);
+        };
+        while (b < b1)
+            each<FMT>(in_turn);
+    } else {
+        for (int b = b0; b < b1; ++b)
+            run(std::integral_constant<int, 0>{}, b);
     }
     wait_vmcnt<0>();
     if constexpr (END == F8_PEERS) {
-        // the item under way, and what the steps of K did not reach, a peer at a time
-        if (item > 0 && b1 - b0 <= items)
-            add_item(item - 1);
+        // the items under way, and what the steps of K did not reach, a peer at a time
+        const int steps = max(b1 - b0, 0), item = min(steps, items);
+        auto under_way = [&](auto c) {
+            constexpr int i = decltype(c)::value;
+#pragma unroll
+            for (int d = 1; d <= SLOTS; ++d) {
+                const int w = steps - d;
+                if (w >= 0 && w < items && w % FMT == i)
+                    add_item(slots + (uint32_t)((w & (SLOTS - 1)) * F8_SLOT), acc[i]);
+            }
+        };
+        each<FMT>(under_way);
         for (int q = item / FMT; q < p.npeers; ++q) {
             u32x2_t w[FMT][4];
 #pragma unroll
             for (int i = 0; i < FMT; ++i) {
-                const uint16_t *from;
-                const uint32_t bytes = peer_at(q * FMT + i, from);
-                const __amdgpu_buffer_rsrc_t rp = make_rsrc(from, q * FMT + i < item ? 0u : bytes);
+                const __amdgpu_buffer_rsrc_t rp =
+                    make_rsrc(p.partials + q * p.peer_stride + part_at + (int64_t)(16 * i) * p.N,
+                              q * FMT + i < item ? 0u : peer_bytes(i));
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     w[i][j] = __builtin_bit_cast(

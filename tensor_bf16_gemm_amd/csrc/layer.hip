@@ -73,7 +73,6 @@ struct Fp8Plan {
 
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, int cus)
 {
-    (void)npeers;
     if (M <= 64)
         return {M <= 16 ? 16 : M <= 32 ? 32 : 64, M <= 16 ? 16 : 32, 1};
     const int blocks = (int)((K + 127) / 128);
