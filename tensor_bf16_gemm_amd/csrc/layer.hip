@@ -311,11 +311,11 @@ int gemm_coll_gemm_fp8(const gc_e4m3 *A, const float *a_scales, int64_t a_row_st
         if (blocks <= 16)
             launch_fp8_stream<1, 1, 4, 4>(a, st);
         else
-            launch_fp8_stream<1, 1, 8, 6>(a, st);
+            launch_fp8_stream<1, 1, 4, 4>(a, st);
     } else if (pl.rows == 32) {
-        launch_fp8_stream<2, 2, 8, 3>(a, st);
+        launch_fp8_stream<2, 2, 4, 4>(a, st);
     } else {
-        launch_fp8_stream<4, 2, 8, 2>(a, st);
+        launch_fp8_stream<4, 2, 4, 2>(a, st);
     }
     return launched();
 }
