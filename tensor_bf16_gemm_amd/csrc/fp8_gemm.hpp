@@ -28,6 +28,7 @@
 namespace gc {
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) f32x4_t lds_f32x4_t;
 
 struct Fp8Args {
     const uint8_t *A;          // [M][K]
@@ -160,7 +161,9 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fi = lane & 15, fg = lane >> 4;
-    const int nt = blockIdx.x % p.tiles_n, mt = blockIdx.x / p.tiles_n;
+    // (neighbours on an XCD share columns: B passes its L2 once)
+    const int unit = xcd_remap(blockIdx.x, gridDim.x);
+    const int nt = unit / p.tiles_m, mt = unit - nt * p.tiles_m;
     const int m0 = mt * 16 * RB, n0 = nt * 16 * NB;
     const u32x4_t rA = make_rsrc4(p.A, (uint32_t)p.M * (uint32_t)p.K);
     const u32x4_t rB = make_rsrc4(p.B, (uint32_t)p.N * (uint32_t)p.K);
@@ -204,19 +207,28 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
                        on ? (uint32_t)(n0 / 128 * p.blocks + c0 + lane) * 4u : OOB);
     };
 
-    // The peers' part of the blocks that the wave will finish (4 columns of a row
-    // per lane and block), asked for first.
-    constexpr int MINE = (RB * NB + W - 1) / W, EARLY = MINE == 1 ? 7 : 0;
-    u32x2_t early[EARLY > 0 ? EARLY : 1];
-    {
-        const int m = m0 + 16 * (wave / NB) + fi, n = n0 + 16 * (wave % NB) + 4 * fg;
-        const bool in = wave < RB * NB && m < p.M && n < p.N;
-        const int64_t to = (int64_t)m * p.N + n;
+    // The end: a thread takes 8 columns of a row, neighbouring threads a row's
+    // (see above), MINE times.  Its part of the first peers is asked for first.
+    constexpr int PER_ROW = 2 * NB, ITEMS = 16 * RB * PER_ROW, MINE = (ITEMS + 64 * W - 1) / (64 * W);
+    constexpr int EARLY = MINE == 1 ? 7 : 4;
+    u32x4_t early[MINE][EARLY];
+    auto place = [&](int k, int &row, int &col, int64_t &to) {     // whether there is a k-th, and where
+        const int item = tid + 64 * W * k;
+        row = item / PER_ROW;
+        col = 8 * (item % PER_ROW);
+        to = (int64_t)(m0 + row) * p.N + n0 + col;
+        return item < ITEMS && m0 + row < p.M && n0 + col < p.N;
+    };
+#pragma unroll
+    for (int k = 0; k < MINE; ++k) {
+        int row, col;
+        int64_t to;
+        const bool in = place(k, row, col, to);
 #pragma unroll
         for (int q = 0; q < EARLY; ++q) {
-            early[q] = (u32x2_t){0u, 0u};
+            early[k][q] = (u32x4_t){0u, 0u, 0u, 0u};
             if (q < p.npeers && in)
-                early[q] = *(const u32x2_t *)(p.partials + q * p.peer_stride + to);
+                early[k][q] = __builtin_nontemporal_load((const u32x4_t *)(p.partials + q * p.peer_stride + to));
         }
     }
     f32x4_t acc[RB][NB];
@@ -267,23 +279,28 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
         for (int j = 0; j < NB; ++j)
             sums[((wave * RB + i) * NB + j) * 64 + lane] = acc[i][j];
     __syncthreads();
-    for (int c = wave; c < RB * NB; c += W) {
-        const int i = c / NB, j = c - i * NB;
-        f32x4_t x = sums[c * 64 + lane];
 #pragma unroll
-        for (int w = 1; w < W; ++w)
-            x += sums[(w * RB * NB + c) * 64 + lane];
-        const int m = m0 + 16 * i + fi, n = n0 + 16 * j + 4 * fg;
-        if (m >= p.M || n >= p.N)
+    for (int k = 0; k < MINE; ++k) {
+        int row, col;
+        int64_t to;
+        if (!place(k, row, col, to))
             continue;
-        const int64_t to = (int64_t)m * p.N + n;
+        // the row's lanes of block (row / 16, col / 16) that hold the 8 columns
+        const int at = (row / 16 * NB + col / 16) * 64 + row % 16 + 32 * (col / 8 % 2);
+        f32x4_t x = sums[at], y = sums[at + 16];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            x += sums[w * RB * NB * 64 + at];
+            y += sums[w * RB * NB * 64 + at + 16];
+        }
+        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
 #pragma unroll
         for (int q = 0; q < EARLY; ++q)
             if (q < p.npeers)
-                x += unpack_bf16x4(early[q]);
-        for (int q = EARLY; q < p.npeers; ++q)
-            x += unpack_bf16x4(*(const u32x2_t *)(p.partials + q * p.peer_stride + to));
-        *(u32x2_t *)(p.out + to) = pack_bf16x4(x);
+                add8(v, early[k][q]);
+        if (p.npeers > EARLY)
+            add_peers(v, p.partials + EARLY * p.peer_stride, p.peer_stride, p.npeers - EARLY, to);
+        *(u32x4_t *)(p.out + to) = pack_bf16x8(v);
     }
 }
 
@@ -340,7 +357,9 @@ template <int FMT, int END>
 __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 {
     constexpr int BMt = 32 * FMT, F8_A = BMt * 128, F8_STAGE = F8_A + F8_B + F8_SCALES;
-    constexpr int SLOTS = FMT == 8 ? 1 : 2;              // (as LDS has room)
+    // as LDS has room
+    constexpr int SLOTS = FMT == 8 ? 1 : 2;
+    constexpr int S = FMT == 2 || (FMT == 4 && END != F8_PEERS) ? 3 : 2;     // stages
     constexpr int G = FMT >= 4 ? 2 : 1;                  // row blocks of a group
     constexpr int GROUPS = (FMT + G - 1) / G, LOG = GROUPS / 2;
     constexpr int LOR = G * LOG, HIR = FMT - LOR;        // row blocks of a wave in lo, in hi
@@ -349,7 +368,7 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     // of the tile's rows (its two rows of waves), and instructions of a wave.
     constexpr int LO_W = LOR > 2 ? 8 : 2 * LOR, HI_W = HIR > 2 ? 8 : 2 * HIR;
     constexpr int LO_N = LO_W == 8 ? 2 : 1, HI_N = HI_W == 8 ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) uint8_t stages[2 * F8_STAGE + (END == F8_PEERS ? 8 * SLOTS * F8_SLOT : 0)];
+    __shared__ __attribute__((aligned(1024))) uint8_t stages[S * F8_STAGE + (END == F8_PEERS ? 8 * SLOTS * F8_SLOT : 0)];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave >> 2, wn = wave & 3, fi = lane & 15, fg = lane >> 4;
@@ -476,7 +495,7 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     // SLOTS places of the wave's own in LDS, and added at the end of step w + SLOTS.
     // (16-byte chunk c of row r is kept at c ^ (r / 2 % 8), as in a stage.)
     const int items = END == F8_PEERS ? FMT * p.npeers : 0;
-    const uint32_t slots = lds0 + (uint32_t)(2 * F8_STAGE + wave * SLOTS * F8_SLOT);
+    const uint32_t slots = lds0 + (uint32_t)(S * F8_STAGE + wave * SLOTS * F8_SLOT);
     const uint32_t p_slot = (uint32_t)(fi * 128 + (((fg >> 1) ^ ((fi >> 1) & 7)) << 4) + 8 * (fg & 1));
     // Buffer of row block i of a peer whose part of the wave begins at `part`: what
     // is read past a row's end is not stored, past the peer's last row it is 0.
@@ -518,8 +537,15 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     mask_y(b0);
     all_y(lds0);
     all_x(lds0);
-    next_y(b0 + 1);
-    all_y(lds0 + (uint32_t)F8_STAGE);
+#pragma unroll
+    for (int d = 1; d < S; ++d) {
+        next_y(b0 + d);
+        all_y(lds0 + (uint32_t)(d * F8_STAGE));
+        if (d < S - 1) {
+            next_x(b0 + d);
+            all_x(lds0 + (uint32_t)(d * F8_STAGE));
+        }
+    }
     wait_vmcnt<0>();
     barrier_only();
     i32x8_t fb[4], fa[2][G];
@@ -537,17 +563,21 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     auto run = [&](auto uc, int b) {
         [[maybe_unused]] constexpr int U = decltype(uc)::value;
         const uint32_t st = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
-        cur ^= 1;
+        const uint32_t before = opaque(lds0 + (uint32_t)((cur == 0 ? S - 1 : cur - 1) * F8_STAGE));
+        cur = cur == S - 1 ? 0 : cur + 1;
         const uint32_t other = opaque(lds0 + (uint32_t)(cur * F8_STAGE));
-        next_x(b + 1);
-        next_y(b + 2);
-        // X: hi of this step has landed
+        next_x(b + S - 1);
+        next_y(b + S);
+        // X: hi of this step has landed.  Younger are the loads after Y of the S - 1
+        // steps before, hi's of S - 2 of them, and (with two stages; else they are
+        // waited for) the item asked for.
         const int step = b - b0;
-        const bool asked = END == F8_PEERS && step > 0 && step <= items;     // an item, at the end of the step before
-        if (asked)
-            wait_either<Y_N + 2, Y_N - LO_N + 2>(lo_on);
+        const bool asked = END == F8_PEERS && S == 2 && step > 0 && step <= items;     // an item, at the end of the step before
+        constexpr int XA = (S - 1) * Y_N + (S - 2) * HI_N;
+        if (!(lo_on && hi_on))
+            wait_either<(S - 1) * (Y_N - LO_N) + 2, (S - 1) * (Y_N - LO_N)>(asked);
         else
-            wait_either<Y_N, Y_N - LO_N>(lo_on);
+            wait_either<XA + 2, XA>(asked);
         barrier_only();
         float s[FMT];
         {
@@ -578,10 +608,11 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
 #pragma unroll
                 for (int i = 0; i < FMT; ++i)
                     asm volatile("" : : "v"(s[i]));
-                if (asked && SLOTS == 2)
-                    wait_either<HI_N + 2, 2>(hi_on);
+                constexpr int YA = (S - 2) * Y_N + (S - 1) * HI_N;
+                if (!(lo_on && hi_on))
+                    wait_either<(S - 2) * (Y_N - LO_N) + 2, (S - 2) * (Y_N - LO_N)>(asked && SLOTS == 2);
                 else
-                    wait_either<HI_N, 0>(hi_on);
+                    wait_either<YA + 2, YA>(asked && SLOTS == 2);
                 barrier_only();
             }
             if constexpr (n < COUNT && in == 0) {
@@ -614,7 +645,7 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             // loads: hi of the next step after X, the rest of the one after it after Y
             if constexpr (n < 4 * LOR) {
                 if constexpr (n % 2 == 1 && n / 2 < HI_N)
-                    load_x(other, std::integral_constant<int, n / 2>{});
+                    load_x(before, std::integral_constant<int, n / 2>{});
             } else if constexpr (n < COUNT) {
                 constexpr int k = n - 4 * LOR;
                 if constexpr (k % EVERY == EVERY - 1 && k / EVERY < Y_N)
@@ -651,9 +682,9 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             run(std::integral_constant<int, 0>{}, b);
     }
     wait_vmcnt<0>();
+    [[maybe_unused]] const int steps = max(b1 - b0, 0);
     if constexpr (END == F8_PEERS) {
-        // the items under way, and what the steps of K did not reach, a peer at a time
-        const int steps = max(b1 - b0, 0), item = min(steps, items);
+        // the items under way
         auto under_way = [&](auto c) {
             constexpr int i = decltype(c)::value;
 #pragma unroll
@@ -664,49 +695,82 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             }
         };
         each<FMT>(under_way);
-        for (int q = item / FMT; q < p.npeers; ++q) {
-            u32x2_t w[FMT][4];
-#pragma unroll
-            for (int i = 0; i < FMT; ++i) {
-                const __amdgpu_buffer_rsrc_t rp =
-                    make_rsrc(p.partials + q * p.peer_stride + part_at + (int64_t)(16 * i) * p.N,
-                              q * FMT + i < item ? 0u : peer_bytes(i));
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[i][j] = __builtin_bit_cast(
-                        u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
-                                     rp, (int)(((uint32_t)fi * (uint32_t)p.N + 4u * fg) * 2u + 32u * j), 0, 0));
-            }
-#pragma unroll
-            for (int i = 0; i < FMT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    acc[i][j] += unpack_bf16x4(w[i][j]);
-        }
     }
 
+    // The end, a row block at a time: through 4 KiB of LDS of the wave's own (the
+    // 16-byte chunk c of row r at c ^ r) into lanes of 8 columns, eight to a row, so
+    // that peers and output pass in whole 128-byte lines.
+    barrier_only();                                      // the stages are read
     const int ln = opaque_v(lane);
-    const int fi2 = ln & 15, fg2 = ln >> 4;
+    const int fi2 = ln & 15, fg2 = ln >> 4, row = ln >> 3, c8 = ln & 7;
+    const uint32_t box = lds0 + (uint32_t)(wave * 4096);
+    auto end = [&](auto c) {
+        constexpr int i = decltype(c)::value;
 #pragma unroll
-    for (int i = 0; i < FMT; ++i) {
-        const int m = m0 + wm * 16 * FMT + 16 * i + fi2;
+        for (int j = 0; j < 4; ++j)
+            *(lds_f32x4_t *)(uintptr_t)(box + (uint32_t)(fi2 * 256 + (((4 * j + fg2) ^ fi2) << 4))) = acc[i][j];
+        float v[2][8];
+        int64_t at[2];
+        bool in[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int n = n0 + 64 * wn + 32 * h + pair_col(fg2);
-            float v[8];
-            pair_f32(acc[i][2 * h], acc[i][2 * h + 1], v);
-            if (m >= p.M || n >= p.N)
-                continue;
-            const int64_t at = (int64_t)m * p.N + n;
-            if constexpr (END == F8_SUMS) {
-                float *to = p.sums + (size_t)pc * p.M * p.N + at;
-                *(f32x4_t *)to = (f32x4_t){v[0], v[1], v[2], v[3]};
-                *(f32x4_t *)(to + 4) = (f32x4_t){v[4], v[5], v[6], v[7]};
-            } else {
-                *(u32x4_t *)(p.out + at) = pack_bf16x8(v);
+            const int r = 8 * h + row, m = m0 + 16 * (FMT * wm + i) + r, n = n0 + 64 * wn + 8 * c8;
+            at[h] = (int64_t)m * p.N + n;
+            in[h] = m < p.M && n < p.N;
+        }
+        // the peers that the steps of K did not reach
+        constexpr int EARLY = 7;
+        u32x4_t peer[END == F8_PEERS ? EARLY : 1][2];
+        const int q0 = steps > i ? min((steps - i - 1) / FMT + 1, p.npeers) : 0;
+        const uint16_t *from = p.partials + q0 * p.peer_stride;
+        const int left = END == F8_PEERS ? p.npeers - q0 : 0;
+        if (left > 0) {
+#pragma unroll
+            for (int q = 0; q < EARLY; ++q)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    peer[q][h] = (u32x4_t){0u, 0u, 0u, 0u};
+                    if (q < left && in[h])
+                        peer[q][h] = __builtin_nontemporal_load((const u32x4_t *)(from + q * p.peer_stride + at[h]));
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = 8 * h + row;
+            const f32x4_t x = *lds_ptr<f32x4_t>(box + (uint32_t)(r * 256 + (((2 * c8) ^ r) << 4)));
+            const f32x4_t y = *lds_ptr<f32x4_t>(box + (uint32_t)(r * 256 + (((2 * c8 + 1) ^ r) << 4)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[h][e] = x[e];
+                v[h][4 + e] = y[e];
             }
         }
-    }
+        if (left > 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int q = 0; q < EARLY; ++q)
+                    if (q < left)
+                        add8(v[h], peer[q][h]);
+                if (left > EARLY && in[h])
+                    add_peers(v[h], from + EARLY * p.peer_stride, p.peer_stride, left - EARLY, at[h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (!in[h])
+                continue;
+            if constexpr (END == F8_SUMS) {
+                float *to = p.sums + (size_t)pc * p.M * p.N + at[h];
+                *(f32x4_t *)to = (f32x4_t){v[h][0], v[h][1], v[h][2], v[h][3]};
+                *(f32x4_t *)(to + 4) = (f32x4_t){v[h][4], v[h][5], v[h][6], v[h][7]};
+            } else {
+                *(u32x4_t *)(p.out + at[h]) = pack_bf16x8(v[h]);
+            }
+        }
+        asm volatile("" : : : "memory");                 // (one row block after the other)
+    };
+    each<FMT>(end);
 }
 
 // out = the sums of all pieces in the order of K, plus the peers, 8 columns a thread.

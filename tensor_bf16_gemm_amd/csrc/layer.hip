@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <utility>
 
 #include "fp8_gemm.hpp"
 #include "gemm_coll_layer.h"
@@ -71,25 +72,51 @@ struct Fp8Plan {
     int rows, cols, splits;
 };
 
+// The cheapest by estimates in us, fitted to 14 sizes (M 100 to 8192, N 1024 to
+// 8192, K 896 to 7168, up to 7 peers) run in every way:
+//   streaming  3.5, and for every round of workgroups 0.8 and their operands'
+//              bytes at 85 GB/s a CU; the weights from HBM at 5.2 TB/s
+//   tiles      3, and for every round 3 and the steps of K: 0.75, 0.87, 1.5 or
+//              1.75 each for 64, 128, 224 or 256 rows (0.85, 1.2, 1.9, 1.95 with
+//              the peers in it)
+//   cut in K   2 to 8 pieces of at least 4 steps: the tiles' steps, 3.5 for the
+//              second launch, and at 6 TB/s the sums, written and read, and the
+//              peers; where the sums have room
+// us measured, streaming / tiles / cut: 16 rows, N 6288, K 7168, 9.4 / - / -; 200
+// rows, N 2048, K 4096, 8.4 / 19 / 16; 256 rows, N 3648, K 7168, 24 / 70 / 22; 512
+// rows, N 6288, K 7168, 7 peers, 92 / 55 / 51; 777 rows, N 3640, K 1040, 27 / 15 /
+// 28; 2048 rows, N 6288, K 7168, 7 peers, - / 113 / 130.
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, int cus)
 {
-    if (M <= 64)
-        return {M <= 16 ? 16 : M <= 32 ? 32 : 64, M <= 16 ? 16 : 32, 1};
-    const int blocks = (int)((K + 127) / 128);
-    Fp8Plan best = {256, 256, 1};
-    double least = 1e30;
-    for (int f : {2, 4, 7, 8}) {
-        const int64_t tiles = (M + 32 * f - 1) / (32 * f) * ((N + 255) / 256);
-        for (int s = 1; s <= 8; ++s) {
-            if (s > 1 && (!workspace || blocks / s < 4 || (int64_t)s * M * N * 4 > kSumBytes))
-                break;
-            const int64_t rounds = (tiles * s + cus - 1) / cus;
-            const double t = (double)rounds * ((blocks + s - 1) / s * (0.5 + 0.1 * f) + 4) +
-                             (s > 1 ? 5 + (double)s * M * N * 8e-6 / 4.0 : 0);
-            if (t < least) {
-                least = t;
-                best = {32 * f, 256, s};
-            }
+    const int64_t blocks = (K + 127) / 128;
+    auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+    Fp8Plan best = {};
+    double least = 1e300;
+    auto take = [&](double t, int rows, int cols, int splits) {
+        if (t < least) {
+            least = t;
+            best = {rows, cols, splits};
+        }
+    };
+    for (const auto &c : {std::pair<int, int>{16, 16}, {16, 32}, {32, 16}, {32, 32}, {32, 64}, {64, 32}}) {
+        if (c.first > 16 && 2 * M <= c.first)
+            continue;                                    // half of the rows would be empty
+        const int64_t units = up(M, c.first) * up(N, c.second);
+        if (units > (int64_t)1 << 20)
+            continue;
+        const double round = 0.8 + (double)(c.first + c.second) * K / 85e3;
+        take(3.5 + std::max((double)up(units, cus) * round, 0.1 * round + (double)N * K / 5.2e6), c.first, c.second, 1);
+    }
+    static const int heights[] = {64, 128, 224, 256};
+    static const double plain[] = {0.75, 0.87, 1.5, 1.75}, peers[] = {0.85, 1.2, 1.9, 1.95};
+    const double bytes = (double)M * N;
+    for (int h = 0; h < 4 && M > 32; ++h) {
+        const int64_t tiles = up(M, heights[h]) * up(N, gc::F8_BN);
+        take(3 + (double)up(tiles, cus) * (3 + blocks * (npeers ? peers : plain)[h]), heights[h], gc::F8_BN, 1);
+        for (int q = 2; workspace && q <= 8 && blocks / q >= 4 && q * M * N * 4 <= kSumBytes; ++q) {
+            const double steps = (double)up(blocks, q) * plain[h];
+            take(6.5 + (double)up(tiles * q, cus) * (3 + steps) + bytes * (8 * q + 2 * npeers) / 6e6, heights[h],
+                 gc::F8_BN, q);
         }
     }
     return best;
@@ -307,15 +334,15 @@ int gemm_coll_gemm_fp8(const gc_e4m3 *A, const float *a_scales, int64_t a_row_st
         case 224: launch_fp8_tiles<7>(a, cus, st); break;
         default: launch_fp8_tiles<8>(a, cus, st); break;
         }
-    } else if (pl.rows == 16) {
-        if (blocks <= 16)
-            launch_fp8_stream<1, 1, 4, 4>(a, st);
-        else
-            launch_fp8_stream<1, 1, 4, 4>(a, st);
-    } else if (pl.rows == 32) {
-        launch_fp8_stream<2, 2, 4, 4>(a, st);
     } else {
-        launch_fp8_stream<4, 2, 4, 2>(a, st);
+        switch (pl.rows * 256 + pl.cols) {
+        case 16 * 256 + 16: launch_fp8_stream<1, 1, 8, 3>(a, st); break;
+        case 16 * 256 + 32: launch_fp8_stream<1, 2, 4, 3>(a, st); break;
+        case 32 * 256 + 16: launch_fp8_stream<2, 1, 4, 3>(a, st); break;
+        case 32 * 256 + 32: launch_fp8_stream<2, 2, 4, 2>(a, st); break;
+        case 32 * 256 + 64: launch_fp8_stream<2, 4, 4, 2>(a, st); break;
+        default: launch_fp8_stream<4, 2, 4, 2>(a, st); break;
+        }
     }
     return launched();
 }

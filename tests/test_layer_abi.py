@@ -124,8 +124,8 @@ def test_fp8_plan():
     assert plan(1, 7168, 896)["tile_cols"] < 256 and plan(16, 6288, 7168)["tile_rows"] == 16
     big = plan(4096, 6288, 7168)
     assert big["tile_cols"] == 256 and big["tile_rows"] >= 192 and big["splits"] == 1
-    assert plan(256, 3648, 7168)["splits"] > 1
-    assert plan(256, 3648, 7168, workspace=False)["splits"] == 1
+    assert plan(256, 6288, 7168, 7)["splits"] > 1
+    assert plan(256, 6288, 7168, 7, workspace=False)["splits"] == 1
     assert plan(0, 64, 64) == dict(tile_rows=0, tile_cols=0, splits=1)
     for bad in (dict(M=-1), dict(K=8), dict(N=4), dict(cus=0), dict(npeers=16)):
         with pytest.raises(RuntimeError):
