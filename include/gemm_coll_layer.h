@@ -7,7 +7,7 @@
  *   gemm_coll_quantize_fp8  bf16 to e4m3 with scales, by rows or by blocks
  *   gemm_coll_gemm_fp8      the product of two e4m3 matrices with scales, plus
  *                           the other ranks' partials
- *   gemm_coll_moe_layer     router, experts and combine for up to 32 tokens in
+ *   gemm_coll_moe_layer     router, experts and combine for up to 16 tokens in
  *                           two launches
  *
  * Conventions are those of gemm_coll.h and gemm_coll_grouped.h: bf16 data,
@@ -48,7 +48,7 @@ extern "C" {
 typedef uint8_t gc_e4m3;
 
 #define GC_NORM_MAX 32768        /* columns of rms_norm */
-#define GC_LAYER_TOKENS_MAX 32   /* tokens of moe_layer */
+#define GC_LAYER_TOKENS_MAX 16   /* tokens of moe_layer */
 
 /*
  * RMS norm.  For each of M rows of N columns

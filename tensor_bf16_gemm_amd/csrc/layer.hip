@@ -126,24 +126,24 @@ Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, in
 // partial tiles of all workgroups.
 constexpr int64_t kMaxMiddle = (int64_t)1 << 24;
 constexpr int kLayerWorkers = 256;                   // workgroups of a launch, at most
-constexpr int64_t kLayerParts = 2 * 16384;           // two partial tiles of 32 x 128
-static_assert(kLayerParts * kLayerWorkers + 8 * gc::ML_PAIRS + 2 * kMaxMiddle <= kSumBytes, "workspace");
+constexpr int64_t kLayerParts = 2 * 8192;            // two partial tiles of 16 x 128
+constexpr int64_t kLayerChosen = (sizeof(gc::Chosen) + 255) / 256 * 256;
+static_assert(kLayerParts * kLayerWorkers + kLayerChosen + 2 * kMaxMiddle <= kSumBytes, "workspace");
 static_assert(kLayerWorkers <= kMaxWorkers, "counters");
 
 // Lanes per token and experts per lane of the router.
-template <int RB, bool BF16>
+template <bool BF16>
 void launch_up(const gc::LayerArgs &a, int grid, hipStream_t st)
 {
     const dim3 g(grid), b(gc::ML_THREADS);
     if (a.route.E <= 64)
-        hipLaunchKernelGGL((gc::moe_up_kernel<RB, 16, 4, BF16>), g, b, 0, st, a);
+        hipLaunchKernelGGL((gc::moe_up_kernel<16, 4, BF16>), g, b, 0, st, a);
     else if (a.route.E <= 256)
-        hipLaunchKernelGGL((gc::moe_up_kernel<RB, 16, 16, BF16>), g, b, 0, st, a);
+        hipLaunchKernelGGL((gc::moe_up_kernel<16, 16, BF16>), g, b, 0, st, a);
     else
-        hipLaunchKernelGGL((gc::moe_up_kernel<RB, 64, 16, BF16>), g, b, 0, st, a);
+        hipLaunchKernelGGL((gc::moe_up_kernel<64, 16, BF16>), g, b, 0, st, a);
 }
 
-template <int RB>
 void launch_layer(gc::LayerArgs &a, bool bf16, int cus, hipStream_t st)
 {
     const int grid = std::min(cus, kLayerWorkers);
@@ -151,11 +151,11 @@ void launch_layer(gc::LayerArgs &a, bool bf16, int cus, hipStream_t st)
     a.min_quads = 4;
     a.tiles_n = (a.F + 63) / 64;
     if (bf16)
-        launch_up<RB, true>(a, grid, st);
+        launch_up<true>(a, grid, st);
     else
-        launch_up<RB, false>(a, grid, st);
+        launch_up<false>(a, grid, st);
     a.tiles_n = (a.N + 127) / 128;
-    hipLaunchKernelGGL((gc::moe_down_kernel<RB>), dim3(grid), dim3(gc::ML_THREADS), 0, st, a);
+    hipLaunchKernelGGL(gc::moe_down_kernel, dim3(grid), dim3(gc::ML_THREADS), 0, st, a);
 }
 
 }  // namespace
@@ -378,7 +378,7 @@ int gemm_coll_moe_layer(const gc_bf16 *X, const void *logits, int logits_type, i
     int cus = 0;
     if (int err = cu_count(cus))
         return err;
-    // Workspace: the counters, the partial tiles, ids and weights, the middle activations.
+    // Workspace: the counters, the partial tiles, who chose what, the middle activations.
     if (workspace_bytes < (uint64_t)base_bytes(cus))
         return GC_EINVAL;
     const int64_t parts = kLayerParts * kLayerWorkers;
@@ -386,9 +386,8 @@ int gemm_coll_moe_layer(const gc_bf16 *X, const void *logits, int logits_type, i
     gc::LayerArgs a = {};
     a.count = (uint32_t *)workspace;
     a.part = (float *)at;
-    a.route.ids = (int32_t *)(at + parts);
-    a.route.weights = (float *)(at + parts + 4 * gc::ML_PAIRS);
-    a.a = (uint16_t *)(at + parts + 8 * gc::ML_PAIRS);
+    a.chosen = (uint32_t *)(at + parts);
+    a.a = (uint16_t *)(at + parts + kLayerChosen);
     const int v = E <= 64 ? 4 : 16;                  // experts of a lane
     a.route.logits = logits;
     a.route.stride = stride;
@@ -414,10 +413,7 @@ int gemm_coll_moe_layer(const gc_bf16 *X, const void *logits, int logits_type, i
     a.F = (int)F;
     a.N = (int)N;
     const hipStream_t st = (hipStream_t)stream;
-    if (T <= 16)
-        launch_layer<1>(a, logits_type == GC_BF16, cus, st);
-    else
-        launch_layer<2>(a, logits_type == GC_BF16, cus, st);
+    launch_layer(a, logits_type == GC_BF16, cus, st);
     return launched();
 }
 

@@ -1,4 +1,4 @@
-// moe_layer.hpp -- gfx950 device code of a layer of experts for up to 32
+// moe_layer.hpp -- gfx950 device code of a layer of experts for up to 16
 // tokens, in two launches:
 //
 //   moe_up_kernel    ids, w = router(logits)
@@ -27,11 +27,12 @@
 
 namespace gc {
 
-constexpr int ML_TOKENS = 32, ML_PAIRS = ML_TOKENS * RT_TOP;
+constexpr int ML_TOKENS = 16, ML_PAIRS = ML_TOKENS * RT_TOP;
 constexpr int ML_THREADS = 256, ML_WAVES = 4, ML_NB = 8, ML_D = 3;
 
 struct LayerArgs {
-    RouteArgs route;           // ids and weights in the workspace
+    RouteArgs route;
+    uint32_t *chosen;          // a Chosen, workspace
     const uint16_t *X;         // [T][K]
     const uint16_t *W1;        // [local][K][2 F]
     const uint16_t *W2;        // [local][F][N]
@@ -49,40 +50,47 @@ struct LayerArgs {
     int part_slots;
 };
 
-// Which tokens chose which of the experts here.
+// Which tokens chose which of the experts here; the first kernel leaves it for
+// the second.
 struct Chosen {
-    uint32_t rows[RT_GROUPS];            // tokens of an expert, a bit each
-    int16_t list[ML_PAIRS];              // experts in use, rising
-    int16_t place[RT_GROUPS];            // an expert's place in the list
+    float w[ML_PAIRS];                   // weights [T][k]
     int8_t slot[ML_PAIRS][ML_TOKENS];    // (place in the list, token): the token's choice that it is, or -1
+    int16_t list[ML_PAIRS];              // experts in use, rising
+    int32_t n, unused;                   // experts in use
+};
+constexpr int ML_WORDS = sizeof(Chosen) / 4;
+
+struct Choice {
+    Chosen kept;
+    uint32_t rows[RT_GROUPS];            // tokens of an expert, a bit each
+    int16_t place[RT_GROUPS];            // an expert's place in the list
     int id[ML_PAIRS];
-    float w[ML_PAIRS];
-    int n;                               // experts in use
 };
 
-// From c.id (of all T * k pairs, in LDS): the rest of c.
-__device__ __forceinline__ void list_experts(Chosen &c, int T, int k, int first, int local)
+// From the ids of all T * k pairs, in LDS: the rest.
+__device__ __forceinline__ void list_experts(Choice &x, int T, int k, int first, int local)
 {
+    Chosen &c = x.kept;
     const int tid = threadIdx.x, lane = tid & 63;
     for (int e = tid; e < local; e += ML_THREADS)
-        c.rows[e] = 0u;
+        x.rows[e] = 0u;
     __syncthreads();
     for (int i = tid; i < T * k; i += ML_THREADS) {
-        const int e = c.id[i] - first;
-        if (c.id[i] >= 0 && (unsigned)e < (unsigned)local)
-            atomicOr(&c.rows[e], 1u << (i / k));
+        const int e = x.id[i] - first;
+        if (x.id[i] >= 0 && (unsigned)e < (unsigned)local)
+            atomicOr(&x.rows[e], 1u << (i / k));
     }
     __syncthreads();
     if (tid < 64) {
         int n = 0;
         for (int e0 = 0; e0 < local; e0 += 64) {
             const int e = e0 + lane;
-            const bool in = e < local && c.rows[e] != 0u;
+            const bool in = e < local && x.rows[e] != 0u;
             const uint64_t all = __builtin_amdgcn_ballot_w64(in);
             if (in) {
                 const int at = n + __builtin_popcountll(all & ((1ull << lane) - 1ull));
                 c.list[at] = (int16_t)e;
-                c.place[e] = (int16_t)at;
+                x.place[e] = (int16_t)at;
             }
             n += __builtin_popcountll(all);
         }
@@ -95,15 +103,15 @@ __device__ __forceinline__ void list_experts(Chosen &c, int T, int k, int first,
         ((uint32_t *)c.slot)[i] = ~0u;
     __syncthreads();
     for (int i = tid; i < T * k; i += ML_THREADS) {
-        const int e = c.id[i] - first;
-        if (c.id[i] >= 0 && (unsigned)e < (unsigned)local)
-            c.slot[c.place[e]][i / k] = (int8_t)(i % k);
+        const int e = x.id[i] - first;
+        if (x.id[i] >= 0 && (unsigned)e < (unsigned)local)
+            c.slot[x.place[e]][i / k] = (int8_t)(i % k);
     }
     __syncthreads();
 }
 
 template <int LPT, int V, bool BF16>
-__device__ __forceinline__ void route_all(const RouteArgs &p, Chosen &c)
+__device__ __forceinline__ void route_all(const RouteArgs &p, Choice &x)
 {
     constexpr int PER = ML_THREADS / LPT;
     using Pair = std::conditional_t<BF16, NarrowPair, WidePair>;
@@ -119,8 +127,8 @@ __device__ __forceinline__ void route_all(const RouteArgs &p, Chosen &c)
         else
             route_token<LPT, V, BF16, false, Pair>(p, tl, j, id, w);
         if (j < p.k && t < p.T) {
-            c.id[t * p.k + j] = id;
-            c.w[t * p.k + j] = w;
+            x.id[t * p.k + j] = id;
+            x.kept.w[t * p.k + j] = w;
         }
     }
     __syncthreads();
@@ -129,24 +137,22 @@ __device__ __forceinline__ void route_all(const RouteArgs &p, Chosen &c)
 // The four waves' sums of RB * NB blocks through LDS, and over the pieces of a
 // tile that is cut: block b's sum by block(b), or by final(x, at, n) once the
 // last workgroup is here.  (As at the end of stream_kernel's tiles.)
-template <int RB>
 struct TileSums {
-    static constexpr int NB = ML_NB, BLOCK = RB * NB * 1024;
+    static constexpr int NB = ML_NB, BLOCK = NB * 1024;
     f32x4_t *sums;
     __amdgpu_buffer_rsrc_t rp;
     uint32_t *count;
     int lane, wave;
+    bool live;                           // the lane's row is a token's
     bool cut;
     int w_first, w_last;
 
-    __device__ __forceinline__ void put(const f32x4_t (&x)[RB][NB])
+    __device__ __forceinline__ void put(const f32x4_t (&x)[NB])
     {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                sums[((wave * RB + i) * NB + j) * 64 + lane] = x[i][j];
+        for (int j = 0; j < NB; ++j)
+            sums[(wave * NB + j) * 64 + lane] = x[j];
         __syncthreads();
     }
     __device__ __forceinline__ f32x4_t block(int b) const
@@ -154,7 +160,7 @@ struct TileSums {
         f32x4_t x = sums[b * 64 + lane];
 #pragma unroll
         for (int w = 1; w < ML_WAVES; ++w)
-            x += sums[(w * RB * NB + b) * 64 + lane];
+            x += sums[(w * NB + b) * 64 + lane];
         return x;
     }
     // Hands piece v of the tile of quads [t0, t0 + per_tile) over; whether it is
@@ -168,9 +174,13 @@ struct TileSums {
         w_first = line.piece_of(t0);
         w_last = line.piece_of(t0 + line.per_tile - 1);
         const uint32_t slot = (uint32_t)(2 * v + (ka == 0 ? 1 : 0));
-        for (int b = wave; b < RB * NB; b += ML_WAVES)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, block(b)), rp,
-                                                   (int)(slot * BLOCK + (uint32_t)(b * 1024 + lane * 16)), 0, CPOL_SYS);
+        for (int b = wave; b < NB; b += ML_WAVES) {
+            const f32x4_t x = block(b);
+            if (live)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, x), rp,
+                                                       (int)(slot * BLOCK + (uint32_t)(b * 1024 + lane * 16)), 0,
+                                                       CPOL_SYS);
+        }
         wait_vmcnt<0>();
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -197,28 +207,35 @@ struct TileSums {
 #pragma unroll
         for (int i = 0; i < N; ++i)
             x[i] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-        for (int w = w_first; w <= w_last; ++w) {
-            const uint32_t slot = (uint32_t)(2 * w + (w == w_first ? 1 : 0));
-            f32x4_t y[N];
+        // AHEAD pieces at a time, in order: every turn is a trip to memory
+        constexpr int AHEAD = 4;
+        for (int w0 = w_first; w0 <= w_last; w0 += AHEAD) {
+            f32x4_t y[AHEAD][N];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                y[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       rp, (int)(slot * BLOCK + (uint32_t)(at[i] * 1024 + lane * 16)),
-                                                       0, CPOL_SYS));
+            for (int d = 0; d < AHEAD; ++d) {
+                const int w = w0 + d;
+                const uint32_t slot = (uint32_t)(2 * w + (w == w_first ? 1 : 0));
+                // (past the last piece: past the buffer)
+                const uint32_t from = live && w <= w_last ? slot * BLOCK + (uint32_t)(lane * 16) : OOB;
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                x[i] += y[i];
+                for (int i = 0; i < N; ++i)
+                    y[d][i] = __builtin_bit_cast(
+                        f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(from + (uint32_t)(at[i] * 1024)), 0, CPOL_SYS));
+            }
+#pragma unroll
+            for (int d = 0; d < AHEAD; ++d)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    x[i] += y[d][i];
         }
     }
 };
 
 // One K-step of a wave from the ring's slot `at`: rows of X against 128 columns.
-template <int RB>
 __device__ __forceinline__ void ring_step(uint32_t at, const uint32_t (&b_frag)[ML_NB], uint32_t a_frag,
-                                          f32x4_t (&acc)[RB][ML_NB])
+                                          f32x4_t (&acc)[ML_NB])
 {
-    bf16x8_t fa[ML_NB], fb[RB];
+    bf16x8_t fa[ML_NB];
 #pragma unroll
     for (int j = 0; j < ML_NB; ++j) {
         bf16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_bf16x4_t *)lds_ptr<bf16x4_t>(at + b_frag[j]));
@@ -226,14 +243,10 @@ __device__ __forceinline__ void ring_step(uint32_t at, const uint32_t (&b_frag)[
             (lds_bf16x4_t *)lds_ptr<bf16x4_t>(at + b_frag[j] + 4 * 256));
         fa[j] = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
     }
+    const bf16x8_t fb = *lds_ptr<bf16x8_t>(at + a_frag);
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
-        fb[i] = *lds_ptr<bf16x8_t>(at + a_frag + i * 1024);
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < ML_NB; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], fb[i], acc[i][j], 0, 0, 0);
+    for (int j = 0; j < ML_NB; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fa[j], fb, acc[j], 0, 0, 0);
 }
 
 // Lane constants of a ring of NB = 8 (see stream_kernel): the 32-byte chunk c
@@ -241,26 +254,25 @@ __device__ __forceinline__ void ring_step(uint32_t at, const uint32_t (&b_frag)[
 __device__ __forceinline__ int ring_fold(int k) { return (k & 3) | (((k >> 3) & 1) << 2); }
 
 // LPT, V: lanes of a token and experts of a lane in the router.
-template <int RB, int LPT, int V, bool BF16>
+template <int LPT, int V, bool BF16>
 __global__ __launch_bounds__(ML_THREADS) void moe_up_kernel(LayerArgs p)
 {
-    constexpr int NB = ML_NB, D = ML_D, B_SLOT = NB * 1024, SLOT = (NB + RB) * 1024, LOADS = NB + RB;
+    constexpr int NB = ML_NB, D = ML_D, B_SLOT = NB * 1024, SLOT = B_SLOT + 1024, LOADS = NB + 1;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[ML_WAVES * D * SLOT];
-    __shared__ Chosen c;
+    __shared__ Choice x;
+    Chosen &c = x.kept;
     __shared__ int s_last;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fi = lane & 15, fg = lane >> 4;
     const int k = p.route.k;
 
-    route_all<LPT, V, BF16>(p.route, c);
+    route_all<LPT, V, BF16>(p.route, x);
+    list_experts(x, p.T, k, p.first, p.local);
     if (blockIdx.x == 0) {
-        for (int i = tid; i < p.T * k; i += ML_THREADS) {
-            p.route.ids[i] = c.id[i];
-            p.route.weights[i] = c.w[i];
-        }
+        for (int i = tid; i < ML_WORDS; i += ML_THREADS)
+            p.chosen[i] = ((const uint32_t *)&c)[i];
     }
-    list_experts(c, p.T, k, p.first, p.local);
     const int tiles = __builtin_amdgcn_readfirstlane(c.n) * p.tiles_n;
     if (tiles <= 0)
         return;
@@ -283,18 +295,15 @@ __global__ __launch_bounds__(ML_THREADS) void moe_up_kernel(LayerArgs p)
     const uint32_t my_ring = lds_addr(ring) + (uint32_t)(wave * D * SLOT);
     const uint32_t N2 = (uint32_t)p.F * 4u;              // bytes of a row of W1
     const u32x4_t rX = make_rsrc4(p.X, (uint32_t)p.T * (uint32_t)p.K * 2u);
-    uint32_t a_off[RB];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-        const int t = 16 * i + (lane >> 2);
-        a_off[i] = t < p.T ? ((uint32_t)t * (uint32_t)p.K + (uint32_t)(8 * a_c)) * 2u : OOB;
-    }
-    TileSums<RB> ts;
+    const int a_tok = lane >> 2;
+    const uint32_t a_off = a_tok < p.T ? ((uint32_t)a_tok * (uint32_t)p.K + (uint32_t)(8 * a_c)) * 2u : OOB;
+    TileSums ts;
     ts.sums = (f32x4_t *)ring;
-    ts.rp = make_rsrc(p.part, (uint32_t)p.part_slots * (uint32_t)TileSums<RB>::BLOCK);
+    ts.rp = make_rsrc(p.part, (uint32_t)p.part_slots * (uint32_t)TileSums::BLOCK);
     ts.count = p.count;
     ts.lane = lane;
     ts.wave = wave;
+    ts.live = fi < p.T;
 
     while (q < q_end) {
         const int t = (int)(q / line.per_tile);
@@ -320,16 +329,12 @@ __global__ __launch_bounds__(ML_THREADS) void moe_up_kernel(LayerArgs p)
 #pragma unroll
             for (int i = 0; i < NB; ++i)
                 dma16(rW, at + i * 1024, on ? b_off[i] + (uint32_t)k0 * N2 : OOB);
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-                dma16(rX, at + B_SLOT + i * 1024, whole ? a_off[i] + (uint32_t)k0 * 2u : OOB);
+            dma16(rX, at + B_SLOT, whole ? a_off + (uint32_t)k0 * 2u : OOB);
         };
-        f32x4_t acc[RB][NB];
+        f32x4_t acc[NB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                acc[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NB; ++j)
+            acc[j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
         int s = ML_WAVES * ka + wave;
 #pragma unroll
         for (int d = 0; d < D - 1; ++d)
@@ -339,45 +344,31 @@ __global__ __launch_bounds__(ML_THREADS) void moe_up_kernel(LayerArgs p)
             wait_lgkmcnt0();                     // the slot to be refilled is read
             issue(s + ML_WAVES * (D - 1), cur == 0 ? D - 1 : cur - 1);
             wait_vmcnt<(D - 1) * LOADS>();       // this step's loads have landed
-            ring_step<RB>(my_ring + cur * SLOT, b_frag, a_frag, acc);
+            ring_step(my_ring + cur * SLOT, b_frag, a_frag, acc);
             cur = cur == D - 1 ? 0 : cur + 1;
         }
         wait_vmcnt<0>();
         ts.put(acc);
         if (!ts.hand_over(line, (int64_t)t * line.per_tile, v, ka, kb, &s_last))
             continue;
-        // Gate and up blocks of 32 columns (pairs u): RB * 2 of them, one a wave and turn.
-        constexpr int UNITS = (RB * 2 + ML_WAVES - 1) / ML_WAVES;
-        f32x4_t x[UNITS * 4];
-        int at[UNITS * 4];
-#pragma unroll
-        for (int n = 0; n < UNITS; ++n) {
-            const int u = min(wave + ML_WAVES * n, RB * 2 - 1), i = u / 2, j = 2 * (u & 1);
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                at[4 * n + d] = i * NB + j + (d & 1) + (d >> 1) * (NB / 2);
-        }
-        ts.final(x, at);
-        const int p8 = 8 * (fg >> 1) + 16 * (fg & 1);
-#pragma unroll
-        for (int n = 0; n < UNITS; ++n) {
-            const int u = wave + ML_WAVES * n, i = u / 2, j = 2 * (u & 1);
-            const u32x4_t pk = pack_pair(silu_mul(x[4 * n], x[4 * n + 2]), silu_mul(x[4 * n + 1], x[4 * n + 3]));
-            const int tok = 16 * i + fi, col = nt * 64 + 16 * j + p8;
-            if (u < RB * 2 && tok < p.T && col < p.F) {
-                const int slot = c.slot[at_list][tok];
-                if (slot >= 0)
-                    *(u32x4_t *)(p.a + (size_t)(tok * k + slot) * p.F + col) = pk;
-            }
+        // Gate and up blocks of 32 columns: two pairs, a wave each.
+        const int j = 2 * (wave & 1);
+        f32x4_t y[4];
+        ts.final(y, {j, j + 1, j + NB / 2, j + NB / 2 + 1});
+        const u32x4_t pk = pack_pair(silu_mul(y[0], y[2]), silu_mul(y[1], y[3]));
+        const int col = nt * 64 + 16 * j + pair_col(fg);
+        if (wave < 2 && fi < p.T && col < p.F) {
+            const int slot = c.slot[at_list][fi];
+            if (slot >= 0)
+                *(u32x4_t *)(p.a + (size_t)(fi * k + slot) * p.F + col) = pk;
         }
         __syncthreads();                         // the ring is free for the next tile
     }
 }
 
-template <int RB>
 __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
 {
-    constexpr int NB = ML_NB, D = ML_D, B_SLOT = NB * 1024, SLOT = (NB + RB) * 1024, LOADS = NB + RB;
+    constexpr int NB = ML_NB, D = ML_D, B_SLOT = NB * 1024, SLOT = B_SLOT + 1024, LOADS = NB + 1;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[ML_WAVES * D * SLOT];
     __shared__ Chosen c;
     __shared__ int s_last;
@@ -385,12 +376,9 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int fi = lane & 15, fg = lane >> 4;
     const int k = p.route.k;
-    for (int i = tid; i < p.T * k; i += ML_THREADS) {
-        c.id[i] = p.route.ids[i];
-        c.w[i] = p.route.weights[i];
-    }
+    for (int i = tid; i < ML_WORDS; i += ML_THREADS)
+        ((uint32_t *)&c)[i] = p.chosen[i];
     __syncthreads();
-    list_experts(c, p.T, k, p.first, p.local);
     const int used = __builtin_amdgcn_readfirstlane(c.n);
     const int KT = (p.F + BK - 1) / BK, quads = max((KT + ML_WAVES - 1) / ML_WAVES, 1);   // of one expert
     // (no expert: the tiles are still written, from the peers alone)
@@ -412,12 +400,13 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
     const uint32_t my_ring = lds_addr(ring) + (uint32_t)(wave * D * SLOT);
     const uint32_t N2 = (uint32_t)p.N * 2u;
     const u32x4_t rA = make_rsrc4(p.a, (uint32_t)(p.T * k) * (uint32_t)p.F * 2u);
-    TileSums<RB> ts;
+    TileSums ts;
     ts.sums = (f32x4_t *)ring;
-    ts.rp = make_rsrc(p.part, (uint32_t)p.part_slots * (uint32_t)TileSums<RB>::BLOCK);
+    ts.rp = make_rsrc(p.part, (uint32_t)p.part_slots * (uint32_t)TileSums::BLOCK);
     ts.count = p.count;
     ts.lane = lane;
     ts.wave = wave;
+    ts.live = fi < p.T;
 
     while (q < q_end) {
         const int t = (int)(q / line.per_tile);
@@ -435,7 +424,8 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
         const int q1 = used > 0 ? kb : 0;
         int ahead = -1, ahead_q = ka, ahead_s = 0;       // loads: expert, quad, step
         u32x4_t rW = {0u, 0u, 0u, 0u};
-        uint32_t a_off[RB] = {};
+        uint32_t a_off = OOB;
+        const int a_tok = lane >> 2;
         auto issue = [&](uint32_t slot) {
             const bool on = ahead_q < q1;
             if (on) {
@@ -445,11 +435,8 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
                     ahead = g;
                     const int e = __builtin_amdgcn_readfirstlane((int)c.list[g]);
                     rW = make_rsrc4(p.W2 + (size_t)e * p.F * p.N, (uint32_t)p.F * N2);
-#pragma unroll
-                    for (int i = 0; i < RB; ++i) {
-                        const int tok = 16 * i + (lane >> 2), j = tok < p.T ? c.slot[g][tok] : -1;
-                        a_off[i] = j >= 0 ? ((uint32_t)(tok * k + j) * (uint32_t)p.F + (uint32_t)(8 * a_c)) * 2u : OOB;
-                    }
+                    const int j = a_tok < p.T ? c.slot[g][a_tok] : -1;
+                    a_off = j >= 0 ? ((uint32_t)(a_tok * k + j) * (uint32_t)p.F + (uint32_t)(8 * a_c)) * 2u : OOB;
                 }
             }
             ++ahead_q;
@@ -463,29 +450,22 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
 #pragma unroll
             for (int i = 0; i < NB; ++i)
                 dma16(r, at + i * 1024, live ? b_off[i] + (uint32_t)k0 * N2 : OOB);
-#pragma unroll
-            for (int i = 0; i < RB; ++i)
-                dma16(rA, at + B_SLOT + i * 1024, whole ? a_off[i] + (uint32_t)k0 * 2u : OOB);
+            dma16(rA, at + B_SLOT, whole ? a_off + (uint32_t)k0 * 2u : OOB);
         };
-        f32x4_t acc[RB][NB], total[RB][NB];
+        f32x4_t acc[NB], total[NB];
 #pragma unroll
-        for (int i = 0; i < RB; ++i)
-#pragma unroll
-            for (int j = 0; j < NB; ++j)
-                acc[i][j] = total[i][j] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < NB; ++n)
+            acc[n] = total[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
         // The sums of expert g of the list enter the rows that chose it.
         auto flush = [&](int g) {
+            const int j = fi < p.T ? c.slot[g][fi] : -1;
+            const float w = j >= 0 ? c.w[fi * k + j] : 0.f;
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const int tok = 16 * i + fi, j = tok < p.T ? c.slot[g][tok] : -1;
-                const float w = j >= 0 ? c.w[tok * k + j] : 0.f;
+            for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int n = 0; n < NB; ++n) {
-#pragma unroll
-                    for (int d = 0; d < 4; ++d)
-                        total[i][n][d] = j >= 0 ? total[i][n][d] + w * acc[i][n][d] : total[i][n][d];
-                    acc[i][n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
-                }
+                for (int d = 0; d < 4; ++d)
+                    total[n][d] = j >= 0 ? total[n][d] + w * acc[n][d] : total[n][d];
+                acc[n] = (f32x4_t){0.f, 0.f, 0.f, 0.f};
             }
         };
 #pragma unroll
@@ -497,7 +477,7 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
             wait_lgkmcnt0();
             issue(cur == 0 ? D - 1 : cur - 1);
             wait_vmcnt<(D - 1) * LOADS>();
-            ring_step<RB>(my_ring + cur * SLOT, b_frag, a_frag, acc);
+            ring_step(my_ring + cur * SLOT, b_frag, a_frag, acc);
             cur = cur == D - 1 ? 0 : cur + 1;
             if (++in == quads || qi + 1 == q1) {
                 flush(g);
@@ -509,27 +489,17 @@ __global__ __launch_bounds__(ML_THREADS) void moe_down_kernel(LayerArgs p)
         ts.put(total);
         if (!ts.hand_over(line, (int64_t)t * line.per_tile, v, ka, kb, &s_last))
             continue;
-        constexpr int UNITS = (RB * 4 + ML_WAVES - 1) / ML_WAVES;
-        f32x4_t x[UNITS * 2];
-        int at[UNITS * 2];
-#pragma unroll
-        for (int n = 0; n < UNITS; ++n) {
-            const int u = wave + ML_WAVES * n, i = u / 4, j = 2 * (u & 3);
-            at[2 * n] = i * NB + j;
-            at[2 * n + 1] = i * NB + j + 1;
-        }
-        ts.final(x, at);
-#pragma unroll
-        for (int n = 0; n < UNITS; ++n) {
-            const int u = wave + ML_WAVES * n, i = u / 4, j = 2 * (u & 3);
-            float o[8];
-            pair_f32(x[2 * n], x[2 * n + 1], o);
-            const int tok = 16 * i + fi, col = t * 128 + 16 * j + pair_col(fg);
-            if (tok < p.T && col < p.N) {
-                const int64_t to = (int64_t)tok * p.N + col;
-                add_peers(o, p.partials, p.peer_stride, p.npeers, to);
-                *(u32x4_t *)(p.out + to) = pack_bf16x8(o);
-            }
+        // Pairs of 32 columns, a wave each.
+        const int j = 2 * wave;
+        f32x4_t x[2];
+        ts.final(x, {j, j + 1});
+        float o[8];
+        pair_f32(x[0], x[1], o);
+        const int col = t * 128 + 16 * j + pair_col(fg);
+        if (fi < p.T && col < p.N) {
+            const int64_t to = (int64_t)fi * p.N + col;
+            add_peers(o, p.partials, p.peer_stride, p.npeers, to);
+            *(u32x4_t *)(p.out + to) = pack_bf16x8(o);
         }
         __syncthreads();                         // the ring is free for the next tile
     }

@@ -4,7 +4,7 @@ include/gemm_coll_layer.h.
     n = rms_norm(x, weight, residual=h, partials=peers, fp8=True)   # n.y e4m3, n.scales, n.sum
     out = gemm_fp8(n.y, n.scales, wq, wq_scales, partials)          # projection + the other ranks' partials
     wq, wq_scales = quantize_fp8(w, block_rows=128)                 # w [N,K], once
-    out = moe_layer(x, logits, w1, w2, k, partials=partials)        # up to 32 tokens
+    out = moe_layer(x, logits, w1, w2, k, partials=partials)        # up to 16 tokens
 
 Tensors, streams, workspaces and errors are as in .grouped, whose workspace
 these calls share.
@@ -75,7 +75,7 @@ def gemm_fp8_plan(M: int, N: int, K: int, npeers: int = 0, *, workspace: bool = 
 def moe_layer(x, logits, w1, w2, k: int, *, first: int = 0, score: str = "softmax", bias=None,
               renormalize: bool = True, scale: float = 1.0, partials=None, out=None, stream=None,
               workspace=None):
-    """A layer of experts for x [T,K], T at most 32, in two launches: the k experts of each token as
+    """A layer of experts for x [T,K], T at most 16, in two launches: the k experts of each token as
     moe_route chooses them from logits [T,E] (score, bias, renormalize, scale likewise), and
     out [T,N] = bf16(sum over the chosen experts that are here of weight * (a . w2[e - first]) + sum
     over p of partials[p]), a = bf16(silu(g) * u), (g, u) the halves of x . w1[e - first].  w1

@@ -110,8 +110,8 @@ LAYER = dict(X=P, logits=P, type=0, stride=64, T=4, E=64, k=8, score=0, bias=Non
                                      (dict(W1=None), EINVAL), (dict(W2=P + 8), EINVAL), (dict(out=P + 8), EINVAL),
                                      (dict(npeers=16), EINVAL), (dict(partials=None), EINVAL),
                                      (dict(pstride=255), EINVAL), (dict(pstride=248), EINVAL),
-                                     (dict(T=33), ENOTSUP), (dict(K=1 << 26), ENOTSUP), (dict(F=1 << 24), ENOTSUP),
-                                     (dict(T=32, k=16, F=(1 << 15) + 8, K=8, N=8), ENOTSUP),
+                                     (dict(T=17), ENOTSUP), (dict(K=1 << 26), ENOTSUP), (dict(F=1 << 24), ENOTSUP),
+                                     (dict(T=16, k=16, F=(1 << 16) + 8, K=8, N=8), ENOTSUP),
                                      (dict(N=1 << 25, F=8), ENOTSUP), (dict(T=0, out=None), OK),
                                      (dict(N=0, out=None), OK)])
 def test_layer_refuses(L, kw, code):

@@ -302,9 +302,9 @@ def check_layer(ins, k, **kw):
 
 @pytest.mark.parametrize("T,E,k,K,F,N", [(1, 1, 1, 8, 8, 8), (1, 8, 2, 64, 40, 72), (1, 64, 8, 1024, 96, 1024),
                                          (2, 3, 5, 40, 24, 136), (5, 60, 6, 1048, 456, 264), (16, 64, 8, 264, 72, 520),
-                                         (17, 16, 4, 520, 128, 128), (32, 64, 8, 256, 136, 384),
-                                         (32, 100, 16, 72, 64, 64), (9, 300, 8, 136, 48, 200),
-                                         (3, 1024, 16, 64, 32, 64), (31, 7, 7, 2048, 320, 1032)])
+                                         (15, 16, 4, 520, 128, 128), (16, 64, 8, 256, 136, 384),
+                                         (16, 100, 16, 72, 64, 64), (9, 300, 8, 136, 48, 200),
+                                         (3, 1024, 16, 64, 32, 64), (13, 7, 7, 2048, 320, 1032)])
 @pytest.mark.parametrize("score,dtype,peers", [("softmax", F32, 0), ("sigmoid", BF16, 3)])
 def test_layer(T, E, k, K, F, N, score, dtype, peers):
     log(f"moe_layer T={T} E={E} k={k} K={K} F={F} N={N} {score} {dtype} peers={peers}")
@@ -315,7 +315,7 @@ def test_layer(T, E, k, K, F, N, score, dtype, peers):
     assert torch.equal(got, again)
 
 
-@pytest.mark.parametrize("T,first,local", [(1, 0, 3), (6, 5, 4), (32, 9, 3), (4, 11, 1)])
+@pytest.mark.parametrize("T,first,local", [(1, 0, 3), (6, 5, 4), (16, 9, 3), (4, 11, 1)])
 def test_layer_of_a_part_of_the_experts(T, first, local):
     check_layer(layer_inputs(T, 12, 3, 136, 72, 264, T, local=local, peers=2), 3, first=first)
 
@@ -385,7 +385,7 @@ def test_layer_of_nothing():
 
 # ---- all of them, as a layer uses them ----
 
-@pytest.mark.parametrize("T", [1, 13, 32])
+@pytest.mark.parametrize("T", [1, 13, 16])
 def test_a_layer(T):
     """The residual stream of one rank through norm, e4m3 projection with its peers, norm, experts
     with their peers, eagerly and as a captured graph that is replayed with other inputs."""
