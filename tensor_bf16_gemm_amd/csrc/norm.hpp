@@ -109,7 +109,7 @@ template <int TPR>
 constexpr int norm_threads() { return TPR < 256 ? 256 : TPR; }
 
 template <int TPR, int V, bool FP8>
-__global__ __launch_bounds__(norm_threads<TPR>()) void norm_kernel(NormArgs p)
+__global__ __launch_bounds__(norm_threads<TPR>(), 4) void norm_kernel(NormArgs p)
 {
     constexpr int NTH = norm_threads<TPR>(), ROWS = NTH / TPR, WPR = TPR / 64;
     __shared__ float part[NTH / 64];
@@ -137,28 +137,38 @@ __global__ __launch_bounds__(norm_threads<TPR>()) void norm_kernel(NormArgs p)
         const bool live = r < p.M;
         const int64_t row = (int64_t)r * p.N;
         float h[V][8] = {};
-        auto add = [&](const uint16_t *src) {
-            u32x4_t raw[V];
+        // BATCH sources at a time, all asked for before the first is added: with few
+        // rows the trips to memory are the time.
+        constexpr int BATCH = V == 1 ? 8 : V == 2 ? 4 : 2;
+        auto add = [&](auto count, auto source) {
+            constexpr int n = decltype(count)::value;
+            u32x4_t raw[n][V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                raw[v] = (u32x4_t){0u, 0u, 0u, 0u};
-                if (live && t + TPR * v < vecs)
-                    raw[v] = *((const u32x4_t *)(src + row) + t + TPR * v);
+            for (int d = 0; d < n; ++d) {
+                const uint16_t *src = source(d);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    raw[d][v] = (u32x4_t){0u, 0u, 0u, 0u};
+                    if (src && live && t + TPR * v < vecs)
+                        raw[d][v] = *((const u32x4_t *)(src + row) + t + TPR * v);
+                }
             }
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                float f[8];
-                unpack8(raw[v], f);
+            for (int d = 0; d < n; ++d)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    h[v][i] += f[i];
-            }
+                for (int v = 0; v < V; ++v) {
+                    float f[8];
+                    unpack8(raw[d][v], f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        h[v][i] += f[i];
+                }
         };
-        add(p.x);
-        if (p.residual)
-            add(p.residual);
-        for (int q = 0; q < p.npeers; ++q)
-            add(p.partials + q * p.peer_stride);
+        add(std::integral_constant<int, 2>{}, [&](int d) { return d == 0 ? p.x : p.residual; });
+        for (int q = 0; q < p.npeers; q += BATCH)
+            add(std::integral_constant<int, BATCH>{}, [&](int d) {
+                return q + d < p.npeers ? p.partials + (q + d) * p.peer_stride : nullptr;
+            });
         float s = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
