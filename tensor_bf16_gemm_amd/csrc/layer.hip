@@ -102,7 +102,7 @@ Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, in
         if (c.first > 16 && 2 * M <= c.first)
             continue;                                    // half of the rows would be empty
         const int64_t units = up(M, c.first) * up(N, c.second);
-        if (units > (int64_t)1 << 20)
+        if (units > (int64_t)1 << 22)                    // (a launch counts its threads in 32 bits)
             continue;
         const double round = 0.8 + (double)(c.first + c.second) * K / 85e3;
         take(3.5 + std::max((double)up(units, cus) * round, 0.1 * round + (double)N * K / 5.2e6), c.first, c.second, 1);

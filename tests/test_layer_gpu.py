@@ -207,6 +207,37 @@ def test_gemm(M, N, K, peers):
     check_gemm(ops, workspace=False)
 
 
+# One size at least for every kind of tile: (rows, columns) of the tile, cut in K or not.
+WAYS = [((16, 16), False, 20, 72, 400), ((16, 32), False, 20, 2056, 656), ((32, 16), False, 450, 264, 656),
+        ((32, 32), False, 40, 3208, 400), ((32, 64), False, 100, 2056, 1040), ((64, 32), False, 4099, 72, 272),
+        ((64, 256), False, 500, 4104, 656), ((128, 256), False, 1800, 2056, 1424), ((128, 256), True, 500, 4104, 4112),
+        ((224, 256), False, 2000, 4104, 400), ((224, 256), False, 1990, 4104, 2192), ((224, 256), True, 1800, 2056, 4112),
+        ((256, 256), False, 2040, 6664, 656), ((256, 256), False, 2047, 6664, 1936)]
+
+
+@pytest.mark.parametrize("tile,cut,M,N,K", WAYS)
+@pytest.mark.parametrize("peers", [0, 1, 9])
+def test_gemm_every_way(tile, cut, M, N, K, peers):
+    """Every kind of tile, with rows, columns and K that end inside one, with more blocks of the
+    peers than steps of K and with fewer (64-bit values on the GPU)."""
+    pl = gc.gemm_fp8_plan(M, N, K, peers)
+    log(f"gemm_fp8 M={M} N={N} K={K} peers={peers} plan {pl}")
+    A, sa, B, sb, p = operands(M, N, K, M + K, peers)
+    want = [t.cpu() for t in ref.gemm(A, sa, B, sb, p)]
+    buf = filled(M + 1, N)
+    got = gc.gemm_fp8(A, sa, B, sb, p, out=buf[:M])
+    ref.check(got, *want, f"{pl}")
+    assert (buf.view(torch.int16)[M] == SENTINEL).all()
+    assert torch.equal(gc.gemm_fp8(A, sa, B, sb, p), got)
+
+
+def test_the_ways_are_taken():
+    """Each size above is run the way it is there for, with or without peers, on 256 compute units."""
+    for tile, cut, M, N, K in WAYS:
+        found = [gc.gemm_fp8_plan(M, N, K, p) for p in (0, 1, 9)]
+        assert any((f["tile_rows"], f["tile_cols"]) == tile and (f["splits"] > 1) == cut for f in found), (tile, found)
+
+
 @pytest.mark.parametrize("M", [3, 70, 300])
 @pytest.mark.parametrize("form", ["columns first", "odd rows", "one for all", "slice"])
 def test_gemm_scales_of_any_strides(M, form):
@@ -256,6 +287,15 @@ def test_gemm_writes_its_rows_only(M):
     assert torch.equal(got, gc.gemm_fp8(A, sa, B, sb, p))
     keep = buf.view(torch.int16)
     assert (keep[0] == SENTINEL).all() and (keep[M + 1:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("M", [4, 100, 700])
+def test_gemm_of_no_columns(M):
+    """K = 0: the peers' sum, whichever way the sizes are run."""
+    p = randn(gen(M), 5, M, 2056).to(DEV)
+    none = lambda n: torch.empty((n, 0), dtype=E4M3, device=DEV)  # noqa: E731
+    got = gc.gemm_fp8(none(M), torch.empty((M, 0), device=DEV), none(2056), torch.empty((17, 0), device=DEV), p)
+    ref.check(got, *ref.combine_peers(p.cpu()), "peers alone")
 
 
 def test_gemm_of_nothing():
@@ -432,3 +472,117 @@ def test_a_layer(T):
             torch.cuda.synchronize()
             for a, b in zip((out[1], out[4], out[5].y, out[5].sum), (want[1], want[4], want[5].y, want[5].sum)):
                 assert torch.equal(a, b), seed
+
+
+# ---- offsets past 32 bits, outputs in larger buffers, refusals ----
+
+@pytest.mark.parametrize("values", ["any bits", "normal"])
+def test_rms_norm_past_four_gigabytes(values):
+    """(Of any bits, the squares' sums overflow and the codes are NaN: bits are compared.)"""
+    M, N = 290_000, 8192                                  # 4.75 GB
+    x = torch.empty((M, N), dtype=BF16, device=DEV)
+    if values == "normal":
+        x.normal_()
+    else:
+        x.view(torch.int16).random_(-16000, 16000)
+    w = torch.ones(N, device=DEV)
+    rows = torch.tensor([0, 131_071, 262_143, 262_144, M - 1], device=DEV)
+    few, bits = x[rows], {E4M3: torch.uint8, F32: torch.int32, BF16: torch.int16}
+    for got, want in ((gc.rms_norm(x, w, residual=x, fp8=True), gc.rms_norm(few, w, residual=few, fp8=True)),
+                      (gc.quantize_fp8(x), gc.quantize_fp8(few))):
+        for a, b in zip(got, want):
+            assert torch.equal(a.view(bits[a.dtype])[rows] if a.dtype != F32 else a[rows].view(torch.int32),
+                               b.contiguous().view(bits[b.dtype]))
+
+
+def test_layer_weights_past_four_gigabytes():
+    T, E, K, F = 3, 130, 4096, 2048                       # w1 4.4 GB
+    x, logits = randn(gen(1), T, K), torch.zeros((T, E))
+    logits[0, 129], logits[1, 0], logits[2, 64] = 9.0, 9.0, 9.0
+    w1 = torch.zeros((E, K, 2 * F), dtype=BF16, device=DEV)
+    w2 = torch.zeros((E, F, 64), dtype=BF16, device=DEV)
+    for e in (0, 64, 129):
+        w1[e], w2[e] = randn(gen(e), K, 2 * F, scale=K ** -0.5).to(DEV), randn(gen(e + 1), F, 64, scale=F ** -0.5).to(DEV)
+    got = gc.moe_layer(x.to(DEV), logits.to(DEV), w1, w2, 1)
+    for t, e in ((0, 129), (1, 0), (2, 64)):
+        one = torch.zeros((1, 1))
+        ref.check(got[t:t + 1], *ref.layer(x[t:t + 1], one, w1[e:e + 1].cpu(), w2[e:e + 1].cpu(), 1), f"expert {e}")
+
+
+@pytest.mark.parametrize("op", ["norm", "norm fp8", "rows", "blocks", "layer"])
+def test_outputs_in_larger_buffers(op):
+    """Outputs of the caller's own are written whole and nothing beside them is."""
+    g = gen(21)
+    M, N = 13, 272
+    x, res, w = dev(randn(g, M, N), randn(g, M, N), randn(g, N))
+    buf, fbuf = filled(M + 2, N), torch.full((M + 2, 8), 7.0, device=DEV)
+    codes = torch.full((M + 2, N), 0x55, dtype=torch.uint8, device=DEV)
+    out, q, s = buf[1:M + 1], codes[1:M + 1].view(E4M3), fbuf[1:M + 1, 2:5]
+    if op == "norm":
+        got = gc.rms_norm(x, w, residual=res, out=out)
+        assert got.y is out and torch.equal(out, gc.rms_norm(x, w, residual=res).y)
+    elif op == "norm fp8":
+        got, want = gc.rms_norm(x, w, residual=res, out=q, scales=s, fp8=True), gc.rms_norm(x, w, residual=res, fp8=True)
+        assert got.y is q and got.scales is s
+        assert torch.equal(codes[1:M + 1], want.y.view(torch.uint8)) and torch.equal(s, want.scales)
+    elif op == "rows":
+        got, want = gc.quantize_fp8(x, out=q, scales=s), gc.quantize_fp8(x)
+        assert got.q is q and torch.equal(codes[1:M + 1], want.q.view(torch.uint8)) and torch.equal(s, want.scales)
+    elif op == "blocks":
+        gc.quantize_fp8(x, block_rows=128, out=q)
+        assert torch.equal(codes[1:M + 1], gc.quantize_fp8(x, block_rows=128).q.view(torch.uint8))
+    else:
+        ins = dev(*layer_inputs(M, 6, 2, 64, 40, N, 3)[:4])
+        assert torch.equal(gc.moe_layer(*ins, 2, out=out), gc.moe_layer(*ins, 2))
+    assert (buf.view(torch.int16)[[0, M + 1]] == SENTINEL).all()
+    assert (codes[[0, M + 1]] == 0x55).all()
+    assert (fbuf[[0, M + 1]] == 7.0).all() and (fbuf[:, :2] == 7.0).all() and (fbuf[:, 5:] == 7.0).all()
+
+
+def test_refusals():
+    g = gen(2)
+    x, res, w = dev(randn(g, 6, 64), randn(g, 6, 64), randn(g, 64))
+    q, s = gc.quantize_fp8(x)
+    b, bs = gc.quantize_fp8(x, block_rows=128)
+    wide = dev(randn(g, 6, 128))[0]
+    for call, what in ((lambda: gc.rms_norm(wide[:, ::2], w), "contiguous"), (lambda: gc.rms_norm(x, w[:32]), "weight"),
+                       (lambda: gc.rms_norm(x, w, residual=res[:5]), "residual"),
+                       (lambda: gc.rms_norm(x, w, partials=res), "partials"),
+                       (lambda: gc.rms_norm(x, w, sum_out=x), "sum_out"), (lambda: gc.rms_norm(x, w, scales=s), "fp8"),
+                       (lambda: gc.rms_norm(x, w, fp8=True, scales=s.expand(6, 1)[:5]), "scales"),
+                       (lambda: gc.rms_norm(x, w, fp8=True, scales=torch.zeros(1, device=DEV).expand(6, 1)), "apart"),
+                       (lambda: gc.quantize_fp8(x, block_rows=64), "block_rows"),
+                       (lambda: gc.gemm_fp8(q, s[:5], b, bs), "a_scales"), (lambda: gc.gemm_fp8(q, s, b, s), "b_scales"),
+                       (lambda: gc.gemm_fp8(q, s.cpu(), b, bs), "device"), (lambda: gc.gemm_fp8(q, s, b[:, :48], bs), "B"),
+                       (lambda: gc.gemm_fp8(q, s, b, bs, out=x), "out"),
+                       (lambda: gc.moe_layer(x, s, x[None], x[None], 1), "w1"),
+                       (lambda: gc.moe_layer(x, s[:5], x[None], x[None], 1), "logits")):
+        with pytest.raises(ValueError, match=what):
+            call()
+    for call in (lambda: gc.rms_norm(x, w.half()), lambda: gc.rms_norm(x, w, out=q), lambda: gc.quantize_fp8(q),
+                 lambda: gc.gemm_fp8(x, s, b, bs), lambda: gc.rms_norm(x, w, residual=res.float())):
+        with pytest.raises(TypeError):
+            call()
+    ins = dev(*layer_inputs(4, 6, 2, 64, 40, 64, 3)[:4])
+    many = dev(*layer_inputs(17, 6, 2, 64, 40, 64, 3)[:4])
+    small = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)
+    for call in (lambda: gc.rms_norm(x, w, eps=-1.0), lambda: gc.rms_norm(x, w, residual=res, out=x, sum_out=x),
+                 lambda: gc.moe_layer(*ins, 2, workspace=False), lambda: gc.moe_layer(*ins, 2, workspace=small),
+                 lambda: gc.moe_layer(*ins, 2, first=1), lambda: gc.moe_layer(*many, 2), lambda: gc.moe_layer(*ins, 17),
+                 lambda: gc.gemm_fp8(q, s, b[:4].contiguous(), bs), lambda: gc.quantize_fp8(x[:, :8].contiguous()),
+                 lambda: gc.gemm_fp8(q, s, torch.cat([b, b[:2]]), bs, workspace=small), lambda: gc.moe_layer(*ins, 0)):
+        with pytest.raises(RuntimeError):
+            call()
+
+
+def test_workspaces_of_the_callers_own():
+    ops = operands(500, 4104, 4112, 4)
+    ws = torch.zeros(gc.grouped_workspace_bytes(), dtype=torch.uint8, device=DEV)
+    assert torch.equal(gc.gemm_fp8(*ops, workspace=ws), gc.gemm_fp8(*ops))
+    ins = dev(*layer_inputs(5, 12, 3, 264, 72, 136, 3)[:4])
+    assert torch.equal(gc.moe_layer(*ins, 3, workspace=ws), gc.moe_layer(*ins, 3))
+    # (the counters are left at zero: a grouped product may take it next)
+    w = ins[2]
+    off = torch.tensor([0] * 5 + [5] * 8, dtype=torch.int32, device=DEV)
+    assert torch.equal(gc.grouped_gemm(ins[0], w, off, workspace=ws), gc.grouped_gemm(ins[0], w, off))
+    assert (ws[:4096] == 0).all()
