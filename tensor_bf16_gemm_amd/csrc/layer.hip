@@ -105,7 +105,8 @@ Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, in
         if (units > (int64_t)1 << 22)                    // (a launch counts its threads in 32 bits)
             continue;
         const double round = 0.8 + (double)(c.first + c.second) * K / 85e3;
-        take(3.5 + std::max((double)up(units, cus) * round, 0.1 * round + (double)N * K / 5.2e6), c.first, c.second, 1);
+        const double rounds = (double)up(units, cus) * round;
+        take(3.5 + std::max(rounds, 0.1 * rounds + (double)N * K / 5.2e6), c.first, c.second, 1);
     }
     static const int heights[] = {64, 128, 224, 256};
     static const double plain[] = {0.75, 0.87, 1.5, 1.75}, peers[] = {0.85, 1.2, 1.9, 1.95};
