@@ -23,8 +23,8 @@
  * columns (the last block of a row may be shorter) of one row, or of 128
  * rows; a value is code * scale.  A block is quantised with
  *   scale = max(largest |value|, 2^-100) / 448
- *   code  = e4m3(value * (448 / max(largest |value|, 2^-100)))
- * in fp32 (codes to nearest-even); a block that holds an infinity or a NaN has
+ *   code  = e4m3(448 * value / max(largest |value|, 2^-100))
+ * in fp32 (codes to nearest-even, the quotient within two units); a block that holds an infinity or a NaN has
  * a scale of NaN and codes of NaN.
  *
  * Peers.  `partials`: npeers (0 to 15) blocks of [M][N], peer_stride elements

@@ -96,6 +96,24 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
     return (u32x4_t){a[0], a[1], b[0], b[1]};
 }
 
+// Eight codes of bf16 values in a block of largest magnitude `top`: the quotient
+// 448 v / top with a step of correction, so that one that lies between two codes
+// stays there and goes to the even one (bf16 values often do; 448 v is exact).
+// Values near the largest float are brought down first, by a power of two.
+__device__ __forceinline__ u32x2_t codes8_bf16(const float (&v)[8], uint32_t most, float inverse)
+{
+    const float down = most >= 0x71800000u ? 0x1p-64f : 1.0f;         // from 2^100 on
+    const float top = __uint_as_float(most < LEAST_BITS ? LEAST_BITS : most) * down;
+    const float inv = inverse / down, part = inv * (1.0f / E4M3_MAX);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float x = v[i] * down, q0 = x * inv;
+        q[i] = __builtin_fmaf(__builtin_fmaf(-q0, top, x * E4M3_MAX), part, q0);
+    }
+    return codes8(q, 1.0f);
+}
+
 // Sum of v over the wave, in every lane.
 __device__ __forceinline__ float wave_sum(float v)
 {
@@ -251,7 +269,7 @@ __global__ __launch_bounds__(QT_THREADS) void quant_rows_kernel(QuantArgs p)
         float inverse;
         const float scale = block_scale(most, inverse);
         if (on)
-            *(u32x2_t *)(p.codes + (int64_t)m * p.K + c) = codes8(v, inverse);
+            *(u32x2_t *)(p.codes + (int64_t)m * p.K + c) = codes8_bf16(v, most, inverse);
         if ((threadIdx.x & 15) == 0)
             p.scales[m * p.scale_stride + b] = scale;
     }
@@ -300,7 +318,7 @@ __global__ __launch_bounds__(QT_THREADS) void quant_blocks_kernel(QuantArgs p)
         float v[8];
         unpack8(raw[i], v);
         if (c < p.K && m < p.M)
-            *(u32x2_t *)(p.codes + (int64_t)m * p.K + c) = codes8(v, inverse);
+            *(u32x2_t *)(p.codes + (int64_t)m * p.K + c) = codes8_bf16(v, most, inverse);
     }
     if (threadIdx.x == 0)
         p.scales[bm * p.scale_stride + bk] = scale;

@@ -155,6 +155,25 @@ def test_quantize_is_exact_where_it_can_be():
 
 
 @pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("power", [0, 100, 119, -80])
+def test_quantize_ties_go_to_the_even_code(rows, power):
+    """Halfway between two codes exactly: the even one, at any size of the block's largest value."""
+    x = torch.zeros((rows, 128))
+    x[0, 0] = 448.0                                       # scale 1 (times the power of two)
+    mid = torch.tensor([17.0, 19.0, 21.0, 23.0, 25.0, 27.0, 29.0, 31.0])      # codes are 16, 18, .. 32 here
+    want = torch.tensor([16.0, 20.0, 20.0, 24.0, 24.0, 28.0, 28.0, 32.0])
+    x[0, 8:16], x[0, 16:24] = mid, -mid
+    top = torch.tensor([448.0 * 3 / 4])                   # 336: quotients 4/3 of the values
+    x2 = torch.zeros((rows, 128))
+    x2[0, 0], x2[0, 8:16] = float(top), mid * 3 / 4
+    for v in (x, x2):
+        q, s = gc.quantize_fp8((v * 2.0 ** power).bfloat16().to(DEV), block_rows=rows)
+        assert torch.equal(q[0, 8:16].float().cpu(), want) and float(q[0, 0]) == 448.0
+    q, s = gc.quantize_fp8((x * 2.0 ** power).bfloat16().to(DEV), block_rows=rows)
+    assert torch.equal(q[0, 16:24].float().cpu(), -want) and float(s[0, 0]) == 2.0 ** power
+
+
+@pytest.mark.parametrize("rows", [1, 128])
 @pytest.mark.parametrize("bad", [NAN, INF, -INF])
 def test_quantize_values_that_are_not_finite(rows, bad):
     """All of a block that holds one is NaN, the other blocks are as without it."""
