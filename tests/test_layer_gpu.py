@@ -497,7 +497,8 @@ def test_a_layer(T):
 
 @pytest.mark.parametrize("values", ["any bits", "normal"])
 def test_rms_norm_past_four_gigabytes(values):
-    """(Of any bits, the squares' sums overflow and the codes are NaN: bits are compared.)"""
+    """(Of any bits, the squares' sums overflow and the codes are NaN: bits are compared,
+    with as many rows as take the same kernel, whose sums have the same order.)"""
     M, N = 290_000, 8192                                  # 4.75 GB
     x = torch.empty((M, N), dtype=BF16, device=DEV)
     if values == "normal":
@@ -506,12 +507,12 @@ def test_rms_norm_past_four_gigabytes(values):
         x.view(torch.int16).random_(-16000, 16000)
     w = torch.ones(N, device=DEV)
     rows = torch.tensor([0, 131_071, 262_143, 262_144, M - 1], device=DEV)
-    few, bits = x[rows], {E4M3: torch.uint8, F32: torch.int32, BF16: torch.int16}
+    few, bits = x[rows].repeat(128, 1), {E4M3: torch.uint8, F32: torch.int32, BF16: torch.int16}
     for got, want in ((gc.rms_norm(x, w, residual=x, fp8=True), gc.rms_norm(few, w, residual=few, fp8=True)),
                       (gc.quantize_fp8(x), gc.quantize_fp8(few))):
         for a, b in zip(got, want):
             assert torch.equal(a.view(bits[a.dtype])[rows] if a.dtype != F32 else a[rows].view(torch.int32),
-                               b.contiguous().view(bits[b.dtype]))
+                               b.contiguous().view(bits[b.dtype])[:5])
 
 
 def test_layer_weights_past_four_gigabytes():
