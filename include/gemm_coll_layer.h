@@ -24,8 +24,8 @@
  * rows; a value is code * scale.  A block is quantised with
  *   scale = max(largest |value|, 2^-100) / 448
  *   code  = e4m3(448 * value / max(largest |value|, 2^-100))
- * in fp32 (codes to nearest-even, the quotient within two units); a block that holds an infinity or a NaN has
- * a scale of NaN and codes of NaN.
+ * in fp32 (codes to nearest-even, the quotient within two units); a block that
+ * holds an infinity or a NaN has a scale of NaN and codes of NaN.
  *
  * Peers.  `partials`: npeers (0 to 15) blocks of [M][N], peer_stride elements
  * apart (a multiple of 8; a row slice of larger partials is a pointer offset
@@ -53,7 +53,8 @@ typedef uint8_t gc_e4m3;
 /*
  * RMS norm.  For each of M rows of N columns
  *   h = x + residual + sum_p partials[p]     (fp32, in that order)
- *   y = h / sqrt(mean(h^2) + eps) * weight   (of h as summed, not as stored)
+ *   y = h / sqrt(mean(h^2) + eps) * weight   (of h as summed, not as stored;
+ *                                             squares beyond fp32 count as infinite)
  * with x, residual (NULL: none) [M][N] and weight [N] of type GC_BF16 or
  * GC_F32.
  *   sum     bf16 [M][N]: h rounded; NULL: not stored; may be x or residual
@@ -84,7 +85,8 @@ int gemm_coll_quantize_fp8(const gc_bf16 *x, int64_t M, int64_t K, int block_row
  * A [M][K], B [N][K] (weights as their checkpoints hold them), out [M][N].
  * a_scales: element (m, b) at m * a_row_stride + b * a_block_stride (fastest
  * with a_block_stride 1 and rows that begin on 16 bytes); b_scales
- * [ceil(N / 128)][ceil(K / 128)].  K a multiple of 16, N of 8.
+ * [ceil(N / 128)][ceil(K / 128)].  K a multiple of 16, N of 8 and below 2^27
+ * (GC_ENOTSUP).
  * The matrix cores add the products of 8 neighbouring k cut off below 2^-13 of
  * the largest of them; all other sums are fp32.  With workspace NULL no product
  * is split along K (slower for few rows); the result differs only by the order
@@ -115,9 +117,8 @@ int gemm_coll_gemm_fp8_plan(int64_t M, int64_t N, int64_t K, int npeers, int wit
  *   a[t][e] = bf16( silu(g) * u ),  (g, u) = X[t] . W1[e - first], halves of 2F
  * X [T][K], W1 [local][K][2F], W2 [local][F][N], out [T][N]; 0 <= T <=
  * GC_LAYER_TOKENS_MAX and T * k * F <= 2^24 (GC_ENOTSUP beyond); K, F and N
- * multiples of 8.  The sums
- * are fp32; an expert that a token has not chosen does not touch its row,
- * whatever its weights hold.  Needs the workspace.
+ * multiples of 8.  The sums are fp32; an expert that a token has not chosen does
+ * not touch its row, whatever its weights hold.  Needs the workspace.
  */
 int gemm_coll_moe_layer(const gc_bf16 *X, const void *logits, int logits_type, int64_t stride, int64_t T,
                         int E, int k, int score, const float *bias, int renormalize, float scale,

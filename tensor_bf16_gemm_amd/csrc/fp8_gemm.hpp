@@ -501,7 +501,7 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
     // is read past a row's end is not stored, past the peer's last row it is 0.
     const int64_t part_at = (int64_t)(m0 + 16 * FMT * wm) * p.N + n0 + 64 * wn;
     auto peer_bytes = [&](int i) {
-        const int rows = min(p.M - (m0 + 16 * (FMT * wm + i)), 16);
+        const int first = m0 + 16 * (FMT * wm + i), rows = min(p.M, first + 16) - min(p.M, first);
         return (uint32_t)max(2 * (rows * p.N - (n0 + 64 * wn)), 0);
     };
     auto ask = [&](const uint16_t *part, int i, uint32_t slot) {

@@ -260,7 +260,7 @@ static int check_fp8(int64_t M, int64_t N, int64_t K, int npeers)
 {
     if (M < 0 || N < 0 || K < 0 || K % 16 != 0 || N % 8 != 0 || npeers < 0 || npeers > 15)
         return GC_EINVAL;
-    if (M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2 || !fits1(M, K) || !fits1(N, K) || !fits(M, N))
+    if (M > INT32_MAX / 2 || N >= 1 << 27 || K > INT32_MAX / 2 || !fits1(M, K) || !fits1(N, K) || !fits(M, N))
         return GC_ENOTSUP;
     return GC_OK;
 }

@@ -132,6 +132,15 @@ def test_fp8_plan():
             plan(**{**dict(M=8, N=64, K=64), **bad})
 
 
+def test_fp8_columns_past_a_launch(L):
+    """Without weights (K 0) only the columns bound a launch: refused, not planned."""
+    with pytest.raises(RuntimeError):
+        gc.gemm_fp8_plan(1, 1 << 28, 0)
+    assert gc.gemm_fp8_plan(1, (1 << 27) - 8, 0)["tile_rows"] == 16
+    assert gc.gemm_fp8_plan(1, (1 << 27) - 16, 16)["tile_rows"] == 16
+    assert L.gemm_coll_gemm_fp8(None, None, 0, 0, None, None, 1, 1 << 28, 0, None, 0, 0, P, None, 0, None) == ENOTSUP
+
+
 def test_plan_struct_layout(tmp_path):
     from tensor_bf16_gemm_amd.layer_abi import Fp8Plan
     names = [n for n, _ in Fp8Plan._fields_]
