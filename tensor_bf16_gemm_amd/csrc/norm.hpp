@@ -102,9 +102,10 @@ __device__ __forceinline__ u32x4_t pack8(const float (&v)[8])
 // Values near the largest float are brought down first, by a power of two.
 __device__ __forceinline__ u32x2_t codes8_bf16(const float (&v)[8], uint32_t most, float inverse)
 {
-    const float down = most >= 0x71800000u ? 0x1p-64f : 1.0f;         // from 2^100 on
+    const bool large = most >= 0x71800000u;              // from 2^100 on
+    const float down = large ? 0x1p-64f : 1.0f, up = large ? 0x1p64f : 1.0f;
     const float top = __uint_as_float(most < LEAST_BITS ? LEAST_BITS : most) * down;
-    const float inv = inverse / down, part = inv * (1.0f / E4M3_MAX);
+    const float inv = inverse * up, part = inv * (1.0f / E4M3_MAX);
     float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
