@@ -124,13 +124,6 @@ __device__ __forceinline__ void add_peers(float (&v)[8], const uint16_t *partial
         add8(v, __builtin_nontemporal_load((const u32x4_t *)(partials + q * stride + at)));
 }
 
-__device__ __forceinline__ u32x4_t pack_bf16x8(const float (&v)[8])
-{
-    const u32x2_t a = pack_bf16x4((f32x4_t){v[0], v[1], v[2], v[3]});
-    const u32x2_t b = pack_bf16x4((f32x4_t){v[4], v[5], v[6], v[7]});
-    return (u32x4_t){a[0], a[1], b[0], b[1]};
-}
-
 // ---- few rows: streaming ----
 //
 // A workgroup of W waves takes 16 * RB rows by 16 * NB columns; its waves take
@@ -143,7 +136,11 @@ __device__ __forceinline__ u32x4_t pack_bf16x8(const float (&v)[8])
 // read a row's 128 bytes.  In the order of the fragments, neighbouring lanes
 // hold neighbouring rows, and such loads pass a CU's address unit at 16 bytes a
 // cycle instead of 64 (38 GB/s per CU against 135, from the L2; 16 rows, N 6288, K
-// 7168: 14.5 us).
+// 7168, 7 peers: 24 us against 9.7, where its 47 MB at the rate of a copy take 9).
+//
+// Bound: the weights' bytes for few rows; with more, what a CU takes in, as every
+// workgroup reads all of its rows of both operands (256 rows, N 3648, K 7168, 7
+// peers: 22 us, 456 workgroups of 32 x 64 on 256 CUs, 85 GB/s a CU).
 //
 // Scales come in chunks of 64 blocks of K, a row's 256 bytes per load (260 apart,
 // so that the 16 rows of a fragment are in different banks).
@@ -314,7 +311,7 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 // The two waves of a SIMD both multiply all the time: a wave alone, whose
 // multiply-adds wait for its own matrix instructions, reaches half the rate (in
 // strict turns, one reading while the other multiplied, 8192 x 8192 x 7168 took
-// 555 us).  Fragments are read one group of row blocks ahead, those of B for
+// 555 us against 402 to 434 now, 2.2 to 2.4 PFLOP/s).  Fragments are read one group of row blocks ahead, those of B for
 // the next step as its last group frees their registers, and loads are asked
 // for between matrix instructions.
 //
@@ -324,6 +321,13 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 // and must have landed at the next X; lo, B and the scales of step b + 2 after Y,
 // to have landed at the next Y: each has a whole step.  What a wave has read it
 // has used before it passes the barrier that lets the place be filled again.
+//
+// Bound: the issue of instructions beside the matrix cores' (a wave gives 317 to
+// 357 in a step of 56 or 64 matrix instructions), and with peers their lines among
+// the stages' loads, which return in order.  4096 x 6288 x 7168 takes 176 to 183 us,
+// 222 to 243 with 7 peers (matrix cores 37 % busy at 2.1 GHz); without the pinned
+// order of a step's instructions 187 for 180.  777 rows, N 3640, K 1040, 3 peers:
+// 17.4, nine steps in one round of 64-row tiles beside their start and end.
 constexpr int F8_THREADS = 512, F8_BN = 256;
 constexpr int F8_B = 256 * 128, F8_SCALES = 5 * 256;
 constexpr int F8_SLOT = 2048;                            // a wave's place for a block of a peer

@@ -234,6 +234,13 @@ __device__ __forceinline__ u32x2_t pack_bf16x4(f32x4_t v)
     return __builtin_bit_cast(u32x2_t, h);
 }
 
+__device__ __forceinline__ u32x4_t pack_bf16x8(const float (&v)[8])
+{
+    const u32x2_t a = pack_bf16x4((f32x4_t){v[0], v[1], v[2], v[3]});
+    const u32x2_t b = pack_bf16x4((f32x4_t){v[4], v[5], v[6], v[7]});
+    return (u32x4_t){a[0], a[1], b[0], b[1]};
+}
+
 // Four bf16 (raw bits in two dwords) -> fp32, exactly.
 // Two neighbouring accumulator blocks of a row block (columns 16j .. 16j+31,
 // j even), packed to bf16 and regrouped so that every lane holds 8

@@ -149,7 +149,7 @@ void launch_layer(gc::LayerArgs &a, bool bf16, int cus, hipStream_t st)
 {
     const int grid = std::min(cus, kLayerWorkers);
     a.part_slots = 2 * grid;
-    a.min_quads = 4;
+    a.min_quads = 4;                                 // (8, 12, 24: one token 73, 76, 96 us; 3: as 4)
     a.tiles_n = (a.F + 63) / 64;
     if (bf16)
         launch_up<true>(a, grid, st);
@@ -203,17 +203,23 @@ int gemm_coll_rms_norm(const gc_bf16 *x, const gc_bf16 *residual, const gc_bf16 
     a.codes = codes;
     a.scales = scales;
     a.scale_stride = scale_stride;
+    // Threads of a row: a wave where one holds it (65536 rows of 512 38 us against 78
+    // with 256 threads, of 1024 90 against 110; few rows the same), then 256, then
+    // 1024.  With at most a row per CU, 1024 threads of one vector from 4097 columns
+    // on: 256 rows of 7168 with 7 peers 6.4 us against 8.6, 16 rows 5.4 against 6.5
+    // (320 rows 11.5 against 11.1, 16384 without peers 167 against 160; up to 4096
+    // columns the same).
     const hipStream_t st = (hipStream_t)stream;
     if (N <= 512)
         launch_norm<64, 1>(a, cus, st);
     else if (N <= 1024)
         launch_norm<64, 2>(a, cus, st);
-    else if (N <= 8192 && M < 2 * cus)
-        launch_norm<1024, 1>(a, cus, st);
     else if (N <= 2048)
         launch_norm<256, 1>(a, cus, st);
     else if (N <= 4096)
         launch_norm<256, 2>(a, cus, st);
+    else if (N <= 8192 && M <= cus)
+        launch_norm<1024, 1>(a, cus, st);
     else if (N <= 8192)
         launch_norm<256, 4>(a, cus, st);
     else if (N <= 16384)
