@@ -667,8 +667,10 @@ __global__ __launch_bounds__(F8_THREADS, 2) void fp8_tile_kernel(Fp8Args p)
             const uint32_t slot = slots + (uint32_t)((step & (SLOTS - 1)) * F8_SLOT);
             if (step >= SLOTS && step - SLOTS < items)
                 add_item(slot, acc[(U + FMT - SLOTS % FMT) % FMT]);
-            if (step < items)
+            if (step < items) {
+                wait_lgkmcnt0();                         // the place is read before it is filled again
                 ask(part, U, slot);
+            }
             if (U == FMT - 1)
                 part += p.peer_stride;
         }
