@@ -204,29 +204,19 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
                        on ? (uint32_t)(n0 / 128 * p.blocks + c0 + lane) * 4u : OOB);
     };
 
-    // The end: a thread takes 8 columns of a row, neighbouring threads a row's
-    // (see above), MINE times.  Its part of the first peers is asked for first.
-    constexpr int PER_ROW = 2 * NB, ITEMS = 16 * RB * PER_ROW, MINE = (ITEMS + 64 * W - 1) / (64 * W);
-    constexpr int EARLY = MINE == 1 ? 7 : 4;
-    u32x4_t early[MINE][EARLY];
-    auto place = [&](int k, int &row, int &col, int64_t &to) {     // whether there is a k-th, and where
-        const int item = tid + 64 * W * k;
-        row = item / PER_ROW;
-        col = 8 * (item % PER_ROW);
-        to = (int64_t)(m0 + row) * p.N + n0 + col;
-        return item < ITEMS && m0 + row < p.M && n0 + col < p.N;
-    };
+    // The end: a thread takes 8 columns of a row, neighbouring threads a row's (see
+    // above).  Its part of the first peers is asked for first.
+    constexpr int PER_ROW = 2 * NB, ITEMS = 16 * RB * PER_ROW, EARLY = 7;
+    static_assert(ITEMS <= 64 * W, "a thread takes one part at most");
+    const int row = tid / PER_ROW, col = 8 * (tid % PER_ROW);
+    const bool mine = tid < ITEMS && m0 + row < p.M && n0 + col < p.N;
+    const int64_t to = (int64_t)(m0 + row) * p.N + n0 + col;
+    u32x4_t early[EARLY];
 #pragma unroll
-    for (int k = 0; k < MINE; ++k) {
-        int row, col;
-        int64_t to;
-        const bool in = place(k, row, col, to);
-#pragma unroll
-        for (int q = 0; q < EARLY; ++q) {
-            early[k][q] = (u32x4_t){0u, 0u, 0u, 0u};
-            if (q < p.npeers && in)
-                early[k][q] = __builtin_nontemporal_load((const u32x4_t *)(p.partials + q * p.peer_stride + to));
-        }
+    for (int q = 0; q < EARLY; ++q) {
+        early[q] = (u32x4_t){0u, 0u, 0u, 0u};
+        if (q < p.npeers && mine)
+            early[q] = __builtin_nontemporal_load((const u32x4_t *)(p.partials + q * p.peer_stride + to));
     }
     f32x4_t acc[RB][NB];
 #pragma unroll
@@ -276,36 +266,31 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
         for (int j = 0; j < NB; ++j)
             sums[((wave * RB + i) * NB + j) * 64 + lane] = acc[i][j];
     __syncthreads();
+    if (!mine)
+        return;
+    // the row's lanes of block (row / 16, col / 16) that hold the 8 columns
+    const int at = (row / 16 * NB + col / 16) * 64 + row % 16 + 32 * (col / 8 % 2);
+    f32x4_t x = sums[at], y = sums[at + 16];
 #pragma unroll
-    for (int k = 0; k < MINE; ++k) {
-        int row, col;
-        int64_t to;
-        if (!place(k, row, col, to))
-            continue;
-        // the row's lanes of block (row / 16, col / 16) that hold the 8 columns
-        const int at = (row / 16 * NB + col / 16) * 64 + row % 16 + 32 * (col / 8 % 2);
-        f32x4_t x = sums[at], y = sums[at + 16];
-#pragma unroll
-        for (int w = 1; w < W; ++w) {
-            x += sums[w * RB * NB * 64 + at];
-            y += sums[w * RB * NB * 64 + at + 16];
-        }
-        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-#pragma unroll
-        for (int q = 0; q < EARLY; ++q)
-            if (q < p.npeers)
-                add8(v, early[k][q]);
-        if (p.npeers > EARLY)
-            add_peers(v, p.partials + EARLY * p.peer_stride, p.peer_stride, p.npeers - EARLY, to);
-        *(u32x4_t *)(p.out + to) = pack_bf16x8(v);
+    for (int w = 1; w < W; ++w) {
+        x += sums[w * RB * NB * 64 + at];
+        y += sums[w * RB * NB * 64 + at + 16];
     }
+    float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+#pragma unroll
+    for (int q = 0; q < EARLY; ++q)
+        if (q < p.npeers)
+            add8(v, early[q]);
+    if (p.npeers > EARLY)
+        add_peers(v, p.partials + EARLY * p.peer_stride, p.peer_stride, p.npeers - EARLY, to);
+    *(u32x4_t *)(p.out + to) = pack_bf16x8(v);
 }
 
 // ---- many rows: tiles through LDS ----
 //
 // Eight waves, 2 along rows and 4 along columns, each 16 * FMT rows by 64
 // columns of a tile of 32 * FMT by 256; one block of K per step, two stages in
-// LDS.  A row of a stage is 128 bytes, its 16-byte chunk c kept at c ^ (row / 2
+// LDS, or three where they fit (see S).  A row of a stage is 128 bytes, its 16-byte chunk c kept at c ^ (row / 2
 // % 8), which spreads the 16 lanes of a fragment read's pass over all 64 banks.
 //
 // The two waves of a SIMD both multiply all the time: a wave alone, whose
@@ -319,8 +304,9 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 // Reads of step b: B and the lower rows of A (lo) after Y of step b - 1, the
 // upper rows (hi) after X of step b.  So hi of step b + 1 is asked for after X
 // and must have landed at the next X; lo, B and the scales of step b + 2 after Y,
-// to have landed at the next Y: each has a whole step.  What a wave has read it
-// has used before it passes the barrier that lets the place be filled again.
+// to have landed at the next Y: each has a whole step (with three stages all are
+// asked for a step earlier and have two).  What a wave has read it has used before
+// it passes the barrier that lets the place be filled again.
 //
 // Bound: the issue of instructions beside the matrix cores' (a wave gives 317 to
 // 357 in a step of 56 or 64 matrix instructions), and with peers their lines among
