@@ -16,7 +16,13 @@
  * bf16 and e4m3 data and 4-byte aligned for float; work enqueued on `stream`,
  * nothing synchronized, no device memory allocated; a negative return launches
  * nothing.  Outputs must not overlap inputs except where it is said.  A buffer
- * addressed as one must be below 2 GiB (GC_ENOTSUP).
+ * addressed as one must be below 2 GiB (GC_ENOTSUP).  Forward only: there are no
+ * gradients, and no backward entry points.
+ *
+ * The kernel is chosen by the sizes and the number of compute units, and the
+ * order of fp32 sums is the kernel's: the same call gives the same bits every
+ * time, but a row's may differ in their last places (a code: by one) from those
+ * of the same row in a call of another number of rows.
  *
  * e4m3.  gc_e4m3 holds the bits of the OCP e4m3 format: finite values up to
  * 448, one NaN per sign, no infinity.  A scale belongs to 128 neighbouring
@@ -24,8 +30,10 @@
  * rows; a value is code * scale.  A block is quantised with
  *   scale = max(largest |value|, 2^-100) / 448
  *   code  = e4m3(448 * value / max(largest |value|, 2^-100))
- * in fp32 (codes to nearest-even, the quotient within two units); a block that
- * holds an infinity or a NaN has a scale of NaN and codes of NaN.
+ * in fp32, codes to nearest-even.  In quantize_fp8 a code is the nearest to the
+ * exact quotient; in rms_norm the quotient is within two units of fp32, so that
+ * one next to the middle of two codes may go to either.  A block that holds an
+ * infinity or a NaN has a scale of NaN and codes of NaN.
  *
  * Peers.  `partials`: npeers (0 to 15) blocks of [M][N], peer_stride elements
  * apart (a multiple of 8; a row slice of larger partials is a pointer offset
@@ -54,7 +62,8 @@ typedef uint8_t gc_e4m3;
  * RMS norm.  For each of M rows of N columns
  *   h = x + residual + sum_p partials[p]     (fp32, in that order)
  *   y = h / sqrt(mean(h^2) + eps) * weight   (of h as summed, not as stored;
- *                                             squares beyond fp32 count as infinite)
+ *                                             squares beyond fp32 count as infinite,
+ *                                             those below its range as zero)
  * with x, residual (NULL: none) [M][N] and weight [N] of type GC_BF16 or
  * GC_F32.
  *   sum     bf16 [M][N]: h rounded; NULL: not stored; may be x or residual
@@ -83,10 +92,11 @@ int gemm_coll_quantize_fp8(const gc_bf16 *x, int64_t M, int64_t K, int block_row
  *                           * sum of A[m][k] * B[n][k] over block b of K
  *                     + sum_p partials[p][m][n] )
  * A [M][K], B [N][K] (weights as their checkpoints hold them), out [M][N].
- * a_scales: element (m, b) at m * a_row_stride + b * a_block_stride (fastest
- * with a_block_stride 1 and rows that begin on 16 bytes); b_scales
- * [ceil(N / 128)][ceil(K / 128)].  K a multiple of 16, N of 8 and below 2^27
- * (GC_ENOTSUP).
+ * a_scales: element (m, b) at m * a_row_stride + b * a_block_stride, any strides
+ * (those of quantize_fp8 and rms_norm, a_block_stride 1, are best for few rows;
+ * for tiles of 256 columns, see the plan below, a_row_stride 1 saves up to 7 %);
+ * b_scales [ceil(N / 128)][ceil(K / 128)].  The product of the two scales is
+ * rounded to fp32 first.  K a multiple of 16, N of 8 and below 2^27 (GC_ENOTSUP).
  * The matrix cores add the products of 8 neighbouring k cut off below 2^-13 of
  * the largest of them; all other sums are fp32.  With workspace NULL no product
  * is split along K (slower for few rows); the result differs only by the order

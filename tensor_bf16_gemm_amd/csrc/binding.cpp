@@ -402,8 +402,8 @@ PyObject *lora_add(PyObject *, PyObject *const *args, Py_ssize_t nargs)
 }
 
 // Scales [rows, ceil(cols / 128)] by rows: the caller's (float32, the columns
-// contiguous), or new ones whose rows begin on 16 bytes, as gemm_fp8 reads them
-// best.
+// contiguous), or new ones whose rows begin on 16 bytes.  (gemm_fp8 reads single
+// scales and takes packed rows as fast.)
 Tensor scales_out(PyObject *o, const Tensor &like, int64_t rows, int64_t cols)
 {
     const int64_t kb = (cols + 127) / 128;

@@ -7,7 +7,9 @@ include/gemm_coll_layer.h.
     out = moe_layer(x, logits, w1, w2, k, partials=partials)        # up to 16 tokens
 
 Tensors, streams, workspaces and errors are as in .grouped, whose workspace
-these calls share.
+these calls share.  Forward only: outputs carry no gradient, also of inputs that
+require one.  A row's result may differ in its last places (a code by one) with
+the number of rows of the call, whose kernel decides the order of its sums.
 """
 from __future__ import annotations
 
@@ -58,9 +60,10 @@ def quantize_fp8(x, *, block_rows: int = 1, out=None, scales=None, stream=None) 
 def gemm_fp8(A, a_scales, B, b_scales, partials=None, out=None, *, stream=None, workspace=None):
     """out [M,N] = bf16(sum over the blocks b of 128 of K of a_scales[m,b] * b_scales[n//128,b] *
     A[m,b] . B[n,b] + sum over p of partials[p]) for e4m3 A [M,K] and B [N,K].  a_scales float32
-    [M,ceil(K/128)] with any strides (rows on 16 bytes with contiguous columns, as quantize_fp8 and
-    rms_norm return them, are fastest); b_scales float32 [ceil(N/128),ceil(K/128)]; partials
-    [npeers,M,N], as for moe_combine.  workspace=False: no product is split along K."""
+    [M,ceil(K/128)] with any strides (contiguous columns, as quantize_fp8 and rms_norm return them, are
+    best for few rows; where gemm_fp8_plan gives tiles of 256 columns, contiguous rows, as of
+    a_scales.t().contiguous().t(), save up to 7 %); b_scales float32 [ceil(N/128),ceil(K/128)];
+    partials [npeers,M,N], as for moe_combine.  workspace=False: no product is split along K."""
     return _on(stream, _native.gemm_fp8, A, a_scales, B, b_scales, partials, out, *_place(A, workspace, 0, stream))
 
 
