@@ -310,8 +310,8 @@ __global__ __launch_bounds__(64 * W) void fp8_stream_kernel(Fp8Args p)
 //
 // Bound: the issue of instructions beside the matrix cores' (a wave gives 317 to
 // 357 in a step of 56 or 64 matrix instructions), and with peers their lines among
-// the stages' loads, which return in order.  4096 x 6288 x 7168 takes 176 to 183 us,
-// 222 to 243 with 7 peers (matrix cores 37 % busy at 2.1 GHz); without the pinned
+// the stages' loads, which return in order.  4096 x 6288 x 7168 takes 176 to 191 us,
+// 222 to 247 with 7 peers (matrix cores 38 % busy at 2 GHz); without the pinned
 // order of a step's instructions 187 for 180.  777 rows, N 3640, K 1040, 3 peers:
 // 17.4, nine steps in one round of 64-row tiles beside their start and end.
 constexpr int F8_THREADS = 512, F8_BN = 256;

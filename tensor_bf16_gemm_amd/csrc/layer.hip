@@ -82,10 +82,12 @@ struct Fp8Plan {
 //   cut in K   2 to 8 pieces of at least 4 steps: the tiles' steps, 3.5 for the
 //              second launch, and at 6 TB/s the sums, written and read, and the
 //              peers; where the sums have room
-// us measured, streaming / tiles / cut: 16 rows, N 6288, K 7168, 9.4 / - / -; 200
-// rows, N 2048, K 4096, 8.4 / 19 / 16; 256 rows, N 3648, K 7168, 24 / 70 / 22; 512
-// rows, N 6288, K 7168, 7 peers, 92 / 55 / 51; 777 rows, N 3640, K 1040, 27 / 15 /
-// 28; 2048 rows, N 6288, K 7168, 7 peers, - / 113 / 130.
+// us measured, the best of each kind, streaming / tiles / cut: N 6288, K 7168, 16
+// rows 9.6 / - / -, 64 rows 12 / 41 / 18, 100 rows 20.8 / 40 / 20.1, 512 rows with 7
+// peers 77 / 55 / 51, 2048 rows with 7 peers 297 / 118 / -; 200 rows, N 2048, K 4096,
+// 8.2 / 25 / 17; 256 rows, N 3648, K 7168, 21 / 42 / 22, with 7 peers 22 / 50 / 25;
+// 777 rows, N 3640, K 1040, 24 / 12.9 / 25, with 3 peers 26 / 17.5 / 28 (estimated
+// 22 / 13.6 / 24).
 Fp8Plan plan_fp8(int64_t M, int64_t N, int64_t K, int npeers, bool workspace, int cus)
 {
     const int64_t blocks = (K + 127) / 128;
@@ -206,9 +208,9 @@ int gemm_coll_rms_norm(const gc_bf16 *x, const gc_bf16 *residual, const gc_bf16 
     // Threads of a row: a wave where one holds it (65536 rows of 512 38 us against 78
     // with 256 threads, of 1024 90 against 110; few rows the same), then 256, then
     // 1024.  With at most a row per CU, 1024 threads of one vector from 4097 columns
-    // on: 256 rows of 7168 with 7 peers 6.4 us against 8.6, 16 rows 5.4 against 6.5
-    // (320 rows 11.5 against 11.1, 16384 without peers 167 against 160; up to 4096
-    // columns the same).
+    // on: calls over changing inputs, rows of 7168, 7 peers, 16 rows 6.3 us against
+    // 8.2, 256 rows 9.7 against 11.6 (320 rows 14.4 against 13.2, 16384 without peers
+    // 169 against 160; up to 4096 columns the same).
     const hipStream_t st = (hipStream_t)stream;
     if (N <= 512)
         launch_norm<64, 1>(a, cus, st);

@@ -6,12 +6,13 @@
 //   moe_down_kernel  out[t] = bf16( sum_j w[t][j] (a[t][j] . W2[ids[t][j]])
 //                                   + sum_p partials[p][t] )
 //
-// The weights of the experts in use are read once and bound both: 16 tokens, 8 of
-// 64 experts, K 7168, F 896, N 7168, 7 peers 374 to 390 us at 5.6 TB/s (2.2 GB); one
-// token 66 to 74 (308 MB, 60 us at the rate of a copy), the rest the routing (1.9
-// us), the list (0.8), the hand-over of cut tiles (2.2 each launch) and the gap
-// between the launches (1.4).  The operators one by one (route, two products,
-// combine) take 71 for one token, 386 for 16.
+// The weights of the experts in use are read once and bound both: over changing
+// inputs, 16 tokens, 8 of 64 experts, K 7168, F 896, N 7168, 7 peers 382 to 396 us at
+// 5.6 TB/s (2.1 to 2.2 GB); one token 74 (308 MB, 60 us at the rate of a copy), the
+// rest the routing (1.9 us), the list (0.8), the hand-over of cut tiles (2.2 each
+// launch) and the gap between the launches (1.4).  The operators one by one (route,
+// two products, combine) take 78 for one token, 394 for 16 in 382; of 256 experts
+// under a biased sigmoid, F 256, 44 for one token in 38, 204 for 16 in 174.
 //
 // With so few tokens a tile's rows are the tokens themselves, all of them for
 // every expert: the matrix cores have rows to spare, and nothing is gathered or

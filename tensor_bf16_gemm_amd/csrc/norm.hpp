@@ -6,7 +6,8 @@
 // HBM bounds both: every input is read once, into registers, and every output
 // written once.  16384 rows of 7168 with a residual to e4m3 take 160 us (826 MB, 5.2
 // TB/s, the rate of a copy), 4096 rows of 7168 quantised 17 us (88 MB), 6288 x 7168
-// by blocks 24 (135 MB); 16 rows with 7 peers 5.4, a launch and two trips to memory.
+// by blocks 24 (135 MB); 16 rows with 7 peers 5.2 in the kernel and 6.3 a call over
+// changing inputs, a launch and two trips to memory.
 // A row is a wave, 256 or 1024 threads (TPR) of V vectors of 8
 // columns each; vector i of a row is thread i % TPR's, so that a wave's loads
 // are whole lines and the 128 columns of a scale are 16 neighbouring lanes: the
